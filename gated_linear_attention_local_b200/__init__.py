@@ -31,6 +31,8 @@ Public functions (same names as the C entry points):
   simple_gla_chunk_bwd(...), simple_gla_fused_recurrent_bwd(...) -- the gradients.
   gla_chunk(q, k, v, gk, ...) -- GLA with a vector gate, chunked form.
   fused_recurrent_simple_gla(...) -- the article's name for simple_gla_fused_recurrent.
+  softmax_attention(...), softmax_attention_fwd / _bwd / _decode_step(...), multi_axis_rotary(...) / _bwd -- the
+      softmax layers of a hybrid model and the rotation of q and k (attention.py).
 """
 from __future__ import annotations
 
@@ -802,3 +804,9 @@ def _size_status(K, V, chunk_size):
     if chunk_size <= 0 or chunk_size & (chunk_size - 1):
         return 1
     return 2
+
+
+from .attention import *  # noqa: E402,F401,F403
+from .attention import __all__ as _attention_all  # noqa: E402
+
+__all__ += _attention_all

@@ -1,0 +1,261 @@
+"""Softmax attention and multi-axis rotary positions: the token mixer of the layers a hybrid model keeps and the
+transform of q and k in front of either mixer ("relinear -- convert pretrained transformers to linear/hybrid-attention
+models").  Argument marshalling for the entry points of ``include/simple_gla.h``, as in the package's ``__init__``.
+
+  softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None) -> o, differentiable
+  softmax_attention_fwd(...) -> (o, lse);  softmax_attention_bwd(q, k, v, o, lse, do, ...) -> {dq, dk, dv}
+  softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, prefix_v=None, scale=None) -> o
+  multi_axis_rotary(q, k, positions, inv_freq, axes=None, interleaved=False) -> (q, k) rotated, differentiable
+  multi_axis_rotary_bwd(dq, dk, positions, inv_freq, ...) -> (dq, dk) rotated back
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _DTYPES, _check_cuda, _on_tensor_device, _ptr, _scale, _stream, _workspace
+from ._lib import lib, raise_for_status
+
+__all__ = ["softmax_attention", "softmax_attention_fwd", "softmax_attention_bwd", "softmax_attention_decode_step",
+           "SoftmaxAttentionFunction", "multi_axis_rotary", "multi_axis_rotary_bwd", "MultiAxisRotaryFunction"]
+
+
+def _operands(named):
+    """CUDA, contiguous, one of the library's two operand types, one type for all."""
+    dtype = None
+    for name, t in named:
+        _check_cuda(name, t)
+        if dtype is None:
+            dtype = t.dtype
+            if dtype not in _DTYPES:
+                raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+        elif t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype} like {named[0][0]}, got {t.dtype}")
+    return _DTYPES[dtype]
+
+
+def _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k):
+    """Checks of the forward and backward; returns (N, Tq, Tk, H, Hk, D, dtype, cu_k)."""
+    dt = _operands((("q", q), ("k", k), ("v", v)))
+    if cu_seqlens is None:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+            raise ValueError("q must be [B,T,H,D] and k, v [B,S,Hk,D]")
+        N = q.shape[0]
+    else:
+        _check_cuda("cu_seqlens", cu_seqlens, torch.int64, 1)
+        _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int64, 1)
+        if q.dim() not in (3, 4) or k.dim() != q.dim():
+            raise ValueError("with cu_seqlens q must be [T,H,D] or [1,T,H,D], and k, v alike")
+        if q.dim() == 4 and (q.shape[0] != 1 or k.shape[0] != 1):
+            raise ValueError("with cu_seqlens the batch size must be 1 (flatten the batch first)")
+        N = cu_seqlens.shape[0] - 1
+        if N < 1:
+            raise ValueError("cu_seqlens must hold at least two entries")
+        if cu_seqlens_k is None:
+            cu_seqlens_k = cu_seqlens
+            if k.shape[-3] != q.shape[-3]:
+                raise ValueError("without cu_seqlens_k, k and v must have as many tokens as q")
+        elif cu_seqlens_k.shape[0] != N + 1:
+            raise ValueError(f"cu_seqlens_k must hold {N + 1} entries like cu_seqlens")
+    if v.shape != k.shape or k.shape[-1] != q.shape[-1]:
+        raise ValueError("k and v must have one shape, and q, k and v one head dimension")
+    H, D = q.shape[-2:]
+    Hk = k.shape[-2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the {H} query heads must be a multiple of the {Hk} key heads")
+    return N, q.shape[-3], k.shape[-3], H, Hk, D, dt, cu_seqlens_k
+
+
+def _check_status(device_status):
+    if device_status is not None:
+        _check_cuda("device_status", device_status, torch.int32)
+        if device_status.numel() < 1:
+            raise ValueError("device_status must hold one element")
+
+
+@_on_tensor_device
+def softmax_attention_fwd(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
+    """Softmax attention.  q [B,T,H,D]; k, v [B,S,Hk,D], H a multiple of Hk; or packed [T,H,D] / [1,T,H,D] with
+    cu_seqlens int64 [N+1] on the device (and cu_seqlens_k where the keys are split otherwise).  causal: query i
+    of a sequence sees the keys j <= i + S - T.  device_status: optional int32 CUDA tensor of one element that
+    receives the cu_seqlens check.  Returns (o shaped like q, lse [..., H] fp32); a query that sees no key has
+    o = 0 and lse = -inf."""
+    N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
+    _check_status(device_status)
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    st = lib().softmax_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _scale(scale), int(bool(causal)), _ptr(o), _ptr(lse),
+                                     _ptr(cu_seqlens), _ptr(cu_k), N, Tq, Tk, H, Hk, D, dt, _ptr(device_status),
+                                     _stream())
+    raise_for_status(st, "softmax_attention_fwd")
+    return o, lse
+
+
+@_on_tensor_device
+def softmax_attention_bwd(q, k, v, o, lse, do, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None,
+                          device_status=None, workspace=None):
+    """Gradients of softmax_attention_fwd for the loss sum(o * do), with its outputs o and lse.  Returns
+    dict(dq, dk, dv) in the shapes and dtype of q, k, v."""
+    N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
+    _check_status(device_status)
+    for name, t in (("o", o), ("do", do)):
+        _check_cuda(name, t, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have the shape of q {tuple(q.shape)}, got {tuple(t.shape)}")
+    _check_cuda("lse", lse, torch.float32)
+    if lse.shape != q.shape[:-1]:
+        raise ValueError(f"lse must be {tuple(q.shape[:-1])}, got {tuple(lse.shape)}")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    nbytes = int(lib().softmax_attention_bwd_workspace_size(q.shape[:-2].numel(), H))
+    ws = _workspace(nbytes, q.device, workspace)
+    st = lib().softmax_attention_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _scale(scale),
+                                     int(bool(causal)), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(cu_seqlens), _ptr(cu_k), N,
+                                     Tq, Tk, H, Hk, D, dt, _ptr(device_status), _ptr(ws), ws.numel(), _stream())
+    raise_for_status(st, "softmax_attention_bwd")
+    return dict(dq=dq, dk=dk, dv=dv)
+
+
+class SoftmaxAttentionFunction(torch.autograd.Function):
+    """softmax_attention_fwd with softmax_attention_bwd as its gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
+        o, lse = softmax_attention_fwd(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
+        ctx.opts = (causal, scale)
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
+        causal, scale = ctx.opts
+        r = softmax_attention_bwd(q, k, v, o, lse, do.contiguous(), causal, scale, cu, cu_k)
+        return r["dq"], r["dk"], r["dv"], None, None, None, None
+
+
+@_on_tensor_device
+def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None):
+    """The output of softmax_attention_fwd alone; differentiable in q, k and v (through softmax_attention_bwd) when
+    gradients are enabled and one of them requires gradients."""
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+    return softmax_attention_fwd(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)[0]
+
+
+@_on_tensor_device
+def softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, prefix_v=None, scale=None, out=None,
+                                  device_status=None, workspace=None):
+    """One token of N sequences: q [N,H,D] against the first lengths[n] tokens (int64 [N] on the device) of
+    k_cache, v_cache [N,S,Hk,D], preceded by prefix_k, prefix_v [P,Hk,D] that all sequences share.  The new
+    token's own key belongs in the cache before the call.  Returns o [N,H,D]."""
+    dt = _operands((("q", q), ("k_cache", k_cache), ("v_cache", v_cache)))
+    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("q must be [N,H,D] and k_cache, v_cache [N,S,Hk,D]")
+    N, H, D = q.shape
+    S, Hk = k_cache.shape[1:3]
+    if k_cache.shape[0] != N or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache must be [{N},S,Hk,{D}], got {tuple(k_cache.shape)}")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the {H} query heads must be a multiple of the {Hk} key heads")
+    _check_cuda("lengths", lengths, torch.int64, 1)
+    if lengths.shape[0] != N:
+        raise ValueError(f"lengths must be [{N}], got {tuple(lengths.shape)}")
+    P = 0
+    if prefix_k is not None or prefix_v is not None:
+        if prefix_k is None or prefix_v is None:
+            raise ValueError("prefix_k and prefix_v go together")
+        for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)):
+            _check_cuda(name, t, q.dtype, 3)
+            if tuple(t.shape[1:]) != (Hk, D):
+                raise ValueError(f"{name} must be [P,{Hk},{D}], got {tuple(t.shape)}")
+        if prefix_k.shape != prefix_v.shape:
+            raise ValueError("prefix_k and prefix_v must have one shape")
+        P = prefix_k.shape[0]
+    _check_status(device_status)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_cuda("out", out, q.dtype, 3)
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
+    nbytes = int(lib().softmax_attention_decode_workspace_size(N, S, P, H, Hk, D, dt))
+    ws = _workspace(nbytes, q.device, workspace) if nbytes or workspace is not None else None
+    st = lib().softmax_attention_decode_step(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
+                                             _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None,
+                                             _scale(scale), _ptr(out), N, S, P, H, Hk, D, dt, _ptr(device_status),
+                                             _ptr(ws), 0 if ws is None else ws.numel(), _stream())
+    raise_for_status(st, "softmax_attention_decode_step")
+    return out
+
+
+def _rotary(q, k, positions, inv_freq, axes, interleaved, inverse, where):
+    dt = _operands((("q", q),) if k is None else (("q", q), ("k", k)))
+    if q.dim() < 2:
+        raise ValueError("q must be [..., H, D]")
+    lead, (H, D) = q.shape[:-2], q.shape[-2:]
+    Hk = 0
+    if k is not None:
+        if k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != D:
+            raise ValueError(f"k must be [..., Hk, D] with q's leading and last dimensions, got {tuple(k.shape)}")
+        Hk = k.shape[-2]
+    _check_cuda("positions", positions, torch.int64)
+    if positions.shape == lead:
+        A = 1
+    elif positions.shape[:-1] == lead and positions.shape[-1] >= 1:
+        A = positions.shape[-1]
+    else:
+        raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead)} + (axes,), got {tuple(positions.shape)}")
+    _check_cuda("inv_freq", inv_freq, torch.float32, 1)
+    half = inv_freq.shape[0]
+    if 2 * half > D:
+        raise ValueError(f"inv_freq has {half} pairs, a head of {D} has {D // 2}")
+    table = bytes(half) if axes is None else bytes(axes)
+    if len(table) != half or (half and max(table) >= A):
+        raise ValueError(f"axes must hold one axis below {A} for each of the {half} pairs")
+    qo = torch.empty_like(q)
+    ko = None if k is None else torch.empty_like(k)
+    st = lib().multi_axis_rotary(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), table, _ptr(qo), _ptr(ko),
+                                 lead.numel(), H, Hk, D, 2 * half, A, int(bool(interleaved)), int(inverse), dt,
+                                 _stream())
+    raise_for_status(st, where)
+    return qo, ko
+
+
+class MultiAxisRotaryFunction(torch.autograd.Function):
+    """multi_axis_rotary with multi_axis_rotary_bwd as its gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, axes, interleaved):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.opts = (axes, interleaved)
+        return _rotary(q, k, positions, inv_freq, axes, interleaved, False, "multi_axis_rotary")
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        positions, inv_freq = ctx.saved_tensors
+        dq, dk = multi_axis_rotary_bwd(dq.contiguous(), None if dk is None else dk.contiguous(), positions, inv_freq,
+                                       *ctx.opts)
+        return dq, dk, None, None, None, None
+
+
+@_on_tensor_device
+def multi_axis_rotary(q, k, positions, inv_freq, axes=None, interleaved=False):
+    """Rotate q [..., H, D] and k [..., Hk, D] (k may be None) by the tokens' positions: pair i of each head turns by
+    positions[..., axes[i]] * inv_freq[i].  positions int64 [..., A], or [...] for one axis; inv_freq fp32 [R/2],
+    R <= D (later columns pass unchanged); axes: R/2 ints, the axis of each pair (None: axis 0).  Pairs are
+    (i, i + R/2), or (2i, 2i + 1) with interleaved.  Returns (q', k'); differentiable in q and k."""
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        return MultiAxisRotaryFunction.apply(q, k, positions, inv_freq, axes, interleaved)
+    return _rotary(q, k, positions, inv_freq, axes, interleaved, False, "multi_axis_rotary")
+
+
+@_on_tensor_device
+def multi_axis_rotary_bwd(dq, dk, positions, inv_freq, axes=None, interleaved=False):
+    """Gradient of multi_axis_rotary: dq, dk rotated by the opposite angles.  Also undoes the rotation."""
+    return _rotary(dq, dk, positions, inv_freq, axes, interleaved, True, "multi_axis_rotary_bwd")

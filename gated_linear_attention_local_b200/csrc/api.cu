@@ -491,6 +491,15 @@ sgla_status launch_status(cudaError_t e, const char *where) {
     return SGLA_OK;
 }
 
+LaunchRecord::LaunchRecord(cudaStream_t st) : st_(st) { prof_mark(st, &begin_); }
+
+sgla_status LaunchRecord::done(cudaError_t e, const char *name) {
+    cudaEvent_t end;
+    prof_mark(st_, &end);
+    prof_push(name, begin_, end);
+    return launch_status(e, name);
+}
+
 sgla_status cuda_failure(cudaError_t e, const char *where) { return cuda_fail(e, where); }
 
 }  // namespace sgla

@@ -14,6 +14,19 @@ namespace sgla {
 // SGLA_ERR_CUDA is returned.
 sgla_status launch_status(cudaError_t e, const char *where);
 
+// One kernel launch of an entry point defined outside api.cu, counted and (while
+// sgla_profile_begin recording is on) timed as those inside it are:
+//   LaunchRecord rec(stream);  status = rec.done(launch(...), "kernel name");
+class LaunchRecord {
+  public:
+    explicit LaunchRecord(cudaStream_t st);
+    sgla_status done(cudaError_t e, const char *name);
+
+  private:
+    cudaStream_t st_;
+    cudaEvent_t begin_;
+};
+
 // A failed CUDA runtime call other than a launch: recorded as above.
 sgla_status cuda_failure(cudaError_t e, const char *where);
 

@@ -1,0 +1,178 @@
+// Rotary positions with several axes, applied to q and k in front of a token mixer
+// ("relinear -- convert pretrained transformers to linear/hybrid-attention models": the
+// layer's _qk_transform rotates q and k; its one-token form is not supported there).
+//
+// Pair i of the R / 2 rotated pairs of a head turns by theta = p * f_i, with p the token's
+// position on the axis of pair i (time, height, width, ... of a patch; one axis for text):
+//   (x, y) <- (x cos theta - y sin theta, x sin theta + y cos theta),
+// pairs (i, i + R/2) or, interleaved, (2 i, 2 i + 1); columns R .. D-1 pass unchanged.  The
+// map is orthogonal, so its gradient is the rotation by -theta.
+//
+// Precision: theta reaches 10^6 and more, where fp32 holds it to 0.06 only.  The turns
+// p * (f_i / 2 pi) are formed in fp64 and reduced to [-1/2, 1/2] there; sine and cosine of
+// the reduced angle are fp32.  Products are fp32, rounded once to the operand type.
+//
+// Bound: HBM (each element read and written once).  cos and sin depend on the token and the
+// pair only, so a block first forms those of its tokens once (shared memory) and then streams
+// every head of q and k past them in 16-byte vectors, two per thread in flight.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch_status.h"
+#include "simple_gla.h"
+
+namespace sgla {
+namespace {
+
+constexpr int kMaxPairs = 256;
+constexpr int kRotThreads = 256;
+
+struct RotArgs {
+    const void *q, *k;
+    void *qo, *ko;
+    const int64_t *pos;
+    const float *freq;
+    int64_t tokens;
+    int H, Hk, D, half, A, tpb;  // half = R / 2 pairs, tpb = tokens per block
+    float sign;
+    uint8_t axis[kMaxPairs];
+};
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Vec {
+    T x[VEC];
+};
+
+// Items of one head: half layout R/2/VEC items of two vectors (the pairs' first and second
+// elements), interleaved R/VEC items of one vector; then (D-R)/VEC vectors that are copied.
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+    extern __shared__ float2 cs[];  // [tpb][half] cos, sin
+    const int64_t t0 = (int64_t)blockIdx.x * a.tpb;
+    const int nt = (int)min64(a.tpb, a.tokens - t0);
+    for (int i = threadIdx.x; i < nt * a.half; i += kRotThreads) {
+        const int t = i / a.half, p = i - t * a.half;
+        double turns = (double)a.pos[(t0 + t) * a.A + a.axis[p]] * ((double)a.freq[p] * 0.15915494309189533577);
+        turns -= rint(turns);
+        float s, c;
+        sincospif(2.f * (float)turns, &s, &c);
+        cs[i] = make_float2(c, a.sign * s);
+    }
+    __syncthreads();
+    using V = Vec<T, VEC>;
+    const int rot_items = INTER ? 2 * a.half / VEC : a.half / VEC;
+    const int per_head = rot_items + (a.D - 2 * a.half) / VEC;
+    const int heads = a.H + a.Hk, per_token = heads * per_head, total = nt * per_token;
+    constexpr int U = 2;
+    for (int base = threadIdx.x; base < total; base += U * kRotThreads) {
+        V x[U], y[U];
+        int64_t off[U];
+        int item[U], tok[U];
+        bool isq[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int idx = base + u * kRotThreads;
+            if (idx >= total) continue;
+            tok[u] = idx / per_token;
+            const int r = idx - tok[u] * per_token, h = r / per_head;
+            item[u] = r - h * per_head;
+            isq[u] = h < a.H;
+            const int col = (INTER || item[u] < rot_items) ? item[u] * VEC : 2 * a.half + (item[u] - rot_items) * VEC;
+            off[u] = (isq[u] ? ((t0 + tok[u]) * a.H + h) : ((t0 + tok[u]) * a.Hk + (h - a.H))) * a.D + col;
+            const T *src = static_cast<const T *>(isq[u] ? a.q : a.k) + off[u];
+            x[u] = *reinterpret_cast<const V *>(src);
+            if (!INTER && item[u] < rot_items) y[u] = *reinterpret_cast<const V *>(src + a.half);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (base + u * kRotThreads >= total) continue;
+            T *dst = static_cast<T *>(isq[u] ? a.qo : a.ko) + off[u];
+            if (item[u] < rot_items) {
+                const float2 *c = cs + tok[u] * a.half + (INTER ? item[u] * VEC / 2 : item[u] * VEC);
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int e = 0; e + 1 < VEC; e += 2) {
+                        const float p = to_f32(x[u].x[e]), r = to_f32(x[u].x[e + 1]);
+                        const float2 w = c[e / 2];
+                        x[u].x[e] = from_f32<T>(p * w.x - r * w.y);
+                        x[u].x[e + 1] = from_f32<T>(p * w.y + r * w.x);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float p = to_f32(x[u].x[e]), r = to_f32(y[u].x[e]);
+                        const float2 w = c[e];
+                        x[u].x[e] = from_f32<T>(p * w.x - r * w.y);
+                        y[u].x[e] = from_f32<T>(p * w.y + r * w.x);
+                    }
+                    *reinterpret_cast<V *>(dst + a.half) = y[u];
+                }
+            }
+            *reinterpret_cast<V *>(dst) = x[u];
+        }
+    }
+}
+
+template <typename T, int VEC>
+cudaError_t launch_rotary(const RotArgs &a, bool inter, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.tokens + a.tpb - 1) / a.tpb);
+    const size_t smem = (size_t)a.tpb * a.half * sizeof(float2);
+    if constexpr (VEC >= 2) {
+        if (inter) {
+            rotary_kernel<T, VEC, true><<<grid, kRotThreads, smem, st>>>(a);
+            return cudaGetLastError();
+        }
+    }
+    rotary_kernel<T, VEC, false><<<grid, kRotThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+// The widest vector that divides every run of columns handled together (at most 16 bytes).
+// D and R are even, so interleaved pairs always fit vectors of two.
+template <typename T>
+cudaError_t launch_rotary_vec(const RotArgs &a, bool inter, cudaStream_t st) {
+    const int run = inter ? (a.D | (2 * a.half)) : (a.D | a.half);  // common low bits of the column offsets
+    if (sizeof(T) == 2 && run % 8 == 0) return launch_rotary<T, 16 / (int)sizeof(T)>(a, inter, st);
+    if (run % 4 == 0) return launch_rotary<T, 4>(a, inter, st);
+    if (run % 2 == 0) return launch_rotary<T, 2>(a, inter, st);
+    return launch_rotary<T, 1>(a, false, st);
+}
+
+}  // namespace
+}  // namespace sgla
+
+extern "C" sgla_status multi_axis_rotary(const void *q, const void *k, const int64_t *positions, const float *inv_freq,
+                                         const uint8_t *axis_of_pair, void *q_out, void *k_out, int64_t tokens,
+                                         int64_t H, int64_t Hk, int64_t D, int64_t R, int64_t A, int interleaved,
+                                         int inverse, sgla_dtype dtype, void *stream) {
+    using namespace sgla;
+    if (tokens < 0 || H < 0 || Hk < 0 || D < 1 || R < 0 || R > D || R % 2 || A < 1)
+        return SGLA_ERR_INVALID_ARGUMENT;
+    if (dtype != SGLA_BF16 && dtype != SGLA_FP32) return SGLA_ERR_INVALID_ARGUMENT;
+    if (D % 2 || R / 2 > kMaxPairs || A > 255 || H + Hk > 65535 || D > 4096 || tokens >= ((int64_t)1 << 31))
+        return SGLA_ERR_UNSUPPORTED;
+    if (tokens == 0 || H + Hk == 0) return SGLA_OK;
+    if ((H > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)) || (R > 0 && (!positions || !inv_freq || !axis_of_pair)))
+        return SGLA_ERR_INVALID_ARGUMENT;
+    for (const void *p : {q, k, (const void *)q_out, (const void *)k_out})
+        if (reinterpret_cast<uintptr_t>(p) % 16) return SGLA_ERR_INVALID_ARGUMENT;
+    if (reinterpret_cast<uintptr_t>(positions) % 8 || reinterpret_cast<uintptr_t>(inv_freq) % 4)
+        return SGLA_ERR_INVALID_ARGUMENT;
+    RotArgs a{};
+    a.q = q; a.k = k; a.qo = q_out; a.ko = k_out; a.pos = positions; a.freq = inv_freq; a.tokens = tokens;
+    a.H = (int)H; a.Hk = (int)Hk; a.D = (int)D; a.half = (int)(R / 2); a.A = (int)A;
+    a.sign = inverse ? -1.f : 1.f;
+    for (int i = 0; i < a.half; ++i) {
+        if (axis_of_pair[i] >= A) return SGLA_ERR_INVALID_ARGUMENT;
+        a.axis[i] = axis_of_pair[i];
+    }
+    // four tokens a block once there are enough blocks to fill the GPU that way, else one
+    a.tpb = tokens >= 4 * 148 * 4 ? 4 : 1;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    LaunchRecord rec(st);
+    return rec.done(dtype == SGLA_BF16 ? launch_rotary_vec<__nv_bfloat16>(a, interleaved != 0, st)
+                                       : launch_rotary_vec<float>(a, interleaved != 0, st),
+                    "multi_axis_rotary");
+}

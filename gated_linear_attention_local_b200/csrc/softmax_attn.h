@@ -1,0 +1,149 @@
+// Softmax attention over heads [tokens, H, D] with shared key heads (internal to
+// libsimplegla.so): arguments and launchers of the forward, backward and one-token kernels.
+//
+//   s_ij = scale q_i . k_j for the keys j that row i sees,  p_i = softmax(s_i),
+//   o_i = sum_j p_ij v_j,  lse_i = log sum_j exp s_ij.
+// Query head h reads key head h / G, G = H / Hk.  A causal row i of a sequence with tq
+// queries and tk keys sees j <= i + tk - tq (the last query is aligned with the last key).
+// A row that sees nothing has o = 0, lse = -inf and gradients 0.
+//
+// A tile's rows are "packed rows" r = token * G + g of one key head: the G query heads that
+// share a key head are rows of the same tile, so every K and V tile is read once for all of
+// them and their dk, dv contributions meet in one accumulator (no atomics, one fixed order).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace sgla {
+
+// The sequences of a call on one side (queries or keys) of the flattened token axis.
+struct AttnSeqs {
+    const int64_t *cu;   // packed: device [N+1]; dense: nullptr
+    const int64_t *len;  // one-token step: device [N] valid keys of each cache; else nullptr
+    int64_t T;           // dense: tokens per sequence; packed: tokens in all
+};
+
+struct AttnArgs {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;           // [q tokens, H], natural log
+    float scale;
+    bool causal, bf16;
+    int64_t N;            // sequences
+    AttnSeqs sq, sk;
+    int H, Hk, G, D;
+    int *status;          // optional device word: SGLA_DEVICE_*
+    // key splits: split z covers keys [z * split, (z + 1) * split); nullptr parts: one split,
+    // o and lse written directly
+    int64_t split;
+    int nsplit;
+    float *part_o;        // [part, q tokens * H, D] o of the split's keys alone
+    float *part_lse;      // [part, q tokens * H]
+    int64_t part_rows;    // q tokens * H
+    // backward
+    const void *dout;
+    const float *lse_in;  // [q tokens, H]
+    float *delta;         // [q tokens, H] sum_d do o
+    void *dq, *dk, *dv;
+};
+
+// CUDA cores
+cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dkdv_simt(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dq_simt(const AttnArgs &a, cudaStream_t st);
+// delta_i = sum_d do_id o_id, one value a row
+cudaError_t launch_attn_delta(const AttnArgs &a, const void *o, cudaStream_t st);
+
+// o of `rows` rows from `parts` parts (part_o, part_lse as in AttnArgs)
+cudaError_t launch_attn_join(const float *part_o, const float *part_lse, void *o, int64_t rows, int parts, int D,
+                             bool bf16, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// The span of sequence n on one side.  Packed batches have one sequence more than the caller
+// gave: index N covers the tokens behind cu[N], which belong to no sequence (their partner
+// span is empty, so their outputs are zeros).  False for bounds that are not
+// 0 <= start <= end <= T.
+__device__ __forceinline__ bool attn_span(const AttnSeqs &s, int64_t N, int64_t n, int64_t &t0, int64_t &len) {
+    if (!s.cu) {
+        t0 = n * s.T;
+        len = s.T;
+        if (s.len) {
+            len = s.len[n];
+            if (len < 0 || len > s.T) return false;
+        }
+        return true;
+    }
+    t0 = s.cu[n];
+    const int64_t t1 = n < N ? s.cu[n + 1] : s.T;
+    len = t1 - t0;
+    return t0 >= 0 && t0 <= t1 && t1 <= s.T;
+}
+
+// Tiles of a packed batch: sequence n starts at slot floor(cu[n] * mul / div) + n, which
+// leaves at least ceil(rows / div) slots for its rows = len * mul and needs no prefix sums;
+// a slot past its sequence's rows has nothing to do.  Slots in all: floor(T * mul / div) + N + 1.
+struct AttnTile {
+    int64_t n;         // sequence
+    int64_t q0, tq;    // its queries
+    int64_t k0, tk;    // its keys
+    int64_t row0;      // first row (own side) of this tile inside the sequence
+};
+
+// Fills t for slot `slot` of the side `own` (sq or sk); all 32 lanes of a warp take part
+// (uniform result).  False: nothing to do.
+__device__ __forceinline__ bool attn_locate(const AttnArgs &a, bool own_q, int64_t slot, int mul, int div,
+                                            AttnTile &t) {
+    const AttnSeqs &own = own_q ? a.sq : a.sk;
+    int64_t first = 0;  // first slot of the sequence
+    if (own.cu && a.status && slot < a.N && (threadIdx.x & 31) == 0) {  // every sequence is checked once, found or not
+        int64_t s0, n0;
+        if (!attn_span(a.sq, a.N, slot, s0, n0) || !attn_span(a.sk, a.N, slot, s0, n0))
+            atomicExch(a.status, kDevBadCuSeqlens);
+    }
+    if (!own.cu) {
+        const int64_t per = (own.T * mul + div - 1) / div;
+        t.n = slot / per;
+        first = t.n * per;
+        if (t.n >= a.N) return false;
+    } else {
+        // largest n in [0, N] whose first slot is <= slot: 32 probes a level
+        const int lane = threadIdx.x & 31;
+        int64_t lo = 0, hi = a.N + 1;  // answer in [lo, hi)
+        while (hi - lo > 1) {
+            const int64_t step = (hi - lo + 31) / 32;
+            const int64_t probe = lo + lane * step;
+            const bool below = probe < hi && own.cu[probe] * mul / div + probe <= slot;
+            const unsigned m = __ballot_sync(0xffffffffu, below);
+            const int c = m == 0u ? 0 : 31 - __clz(m);
+            const int64_t nlo = lo + c * step;
+            hi = min64(hi, nlo + step);
+            lo = nlo;
+        }
+        t.n = lo;
+        first = own.cu[lo] * mul / div + lo;
+    }
+    const bool okq = attn_span(a.sq, a.N, t.n, t.q0, t.tq), okk = attn_span(a.sk, a.N, t.n, t.k0, t.tk);
+    if (!okq || !okk) {
+        if (a.status) atomicExch(a.status, kDevBadCuSeqlens);
+        // a cache whose length is out of range counts as empty; a packed sequence is skipped
+        if (!(okq && a.sk.len)) return false;
+        t.tk = 0;
+    }
+    if (t.n >= a.N) {  // behind the last sequence: zeros
+        if (own_q) t.tk = 0; else t.tq = 0;
+    }
+    t.row0 = (slot - first) * div;
+    return t.row0 >= 0 && t.row0 < (own_q ? t.tq : t.tk) * mul;
+}
+
+__host__ __device__ __forceinline__ int64_t attn_slots(const AttnSeqs &s, int64_t N, int mul, int div) {
+    return s.cu ? s.T * mul / div + N + 1 : N * ((s.T * mul + div - 1) / div);
+}
+
+#endif
+
+}  // namespace sgla

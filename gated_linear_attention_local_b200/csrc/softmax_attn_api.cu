@@ -1,0 +1,224 @@
+// Entry points of softmax attention: argument validation, plan, workspace carve-up and
+// launch order.  Contracts are in include/simple_gla.h.
+#include <math.h>
+
+#include <algorithm>
+
+#include "launch_status.h"
+#include "simple_gla.h"
+#include "softmax_attn.h"
+
+namespace {
+
+using namespace sgla;
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+#define ATTN_LAUNCH(name, call)                       \
+    do {                                              \
+        LaunchRecord rec_(st);                        \
+        const sgla_status s_ = rec_.done(call, name); \
+        if (s_ != SGLA_OK) return s_;                 \
+    } while (0)
+
+sgla_status check_heads(int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype) {
+    if (H < 1 || Hk < 1 || D < 1 || H % Hk) return SGLA_ERR_INVALID_ARGUMENT;
+    if (dtype != SGLA_BF16 && dtype != SGLA_FP32) return SGLA_ERR_INVALID_ARGUMENT;
+    if (D > 128 || D % 8 || H > 65535 || H / Hk > 128) return SGLA_ERR_UNSUPPORTED;
+    return SGLA_OK;
+}
+
+float pick_scale(float scale, int64_t D) {
+    return (!(scale > 0.f) || isinf(scale)) ? 1.0f / sqrtf((float)D) : scale;
+}
+
+sgla_status reset_status(int *device_status, cudaStream_t st) {
+    if (!device_status) return SGLA_OK;
+    const cudaError_t e = cudaMemsetAsync(device_status, 0, sizeof(int), st);
+    return e == cudaSuccess ? SGLA_OK : cuda_failure(e, "status reset");
+}
+
+// Checks shared by the forward and the backward; fills the sequence part of a.
+sgla_status check_seqs(AttnArgs &a, const int64_t *cu_q, const int64_t *cu_k, int64_t N, int64_t Tq, int64_t Tk,
+                       int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype, float scale, int causal,
+                       int *device_status, int64_t &q_tokens, int64_t &k_tokens) {
+    if (N < 0 || Tq < 0 || Tk < 0 || !cu_q != !cu_k || (cu_q && N < 1)) return SGLA_ERR_INVALID_ARGUMENT;
+    const sgla_status s = check_heads(H, Hk, D, dtype);
+    if (s != SGLA_OK) return s;
+    if (Tq >= kMaxTokens || Tk >= kMaxTokens || N >= kMaxTokens) return SGLA_ERR_UNSUPPORTED;
+    q_tokens = cu_q ? Tq : N * Tq;
+    k_tokens = cu_k ? Tk : N * Tk;
+    if (q_tokens >= kMaxTokens || k_tokens >= kMaxTokens) return SGLA_ERR_UNSUPPORTED;
+    if (!aligned(cu_q, 8) || !aligned(cu_k, 8) || !aligned(device_status, 4)) return SGLA_ERR_INVALID_ARGUMENT;
+    a.N = N;
+    a.sq.cu = cu_q; a.sq.T = Tq;
+    a.sk.cu = cu_k; a.sk.T = Tk;
+    a.H = (int)H; a.Hk = (int)Hk; a.G = (int)(H / Hk); a.D = (int)D;
+    a.bf16 = dtype == SGLA_BF16;
+    a.causal = causal != 0;
+    a.scale = pick_scale(scale, D);
+    a.status = device_status;
+    a.split = kMaxTokens;
+    a.nsplit = 1;
+    return SGLA_OK;
+}
+
+// The one-token step: keys are split so that the GPU is filled, the prefix of all sequences
+// is one sequence of N query tokens, and the parts of a row are joined at the end.
+struct DecodePlan {
+    sgla_status why = SGLA_ERR_INVALID_ARGUMENT;
+    int64_t split = 0, psplit = 0;    // keys per part of a cache, of the prefix
+    int parts = 0, pparts = 0;        // parts of a cache, of the prefix
+    bool direct = false;              // one part: no join
+    size_t off_lse = 0, bytes = 0;
+};
+
+int64_t split_keys(int64_t keys, int64_t units) {
+    // enough parts for two CTAs an SM, at least 256 keys each
+    const int64_t want = std::max<int64_t>(1, (2 * 148 + units - 1) / units);
+    const int64_t len = std::max<int64_t>(256, (keys + want - 1) / want);
+    return (len + 63) / 64 * 64;
+}
+
+DecodePlan decode_plan(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype) {
+    DecodePlan p;
+    if (N < 0 || S < 0 || P < 0) return p;
+    if ((p.why = check_heads(H, Hk, D, dtype)) != SGLA_OK) return p;
+    p.why = SGLA_ERR_UNSUPPORTED;
+    if (N >= kMaxTokens || S >= kMaxTokens || P >= kMaxTokens || N * std::max<int64_t>(S, H) >= kMaxTokens) return p;
+    p.why = SGLA_OK;
+    if (N == 0) return p;
+    const int64_t G = H / Hk;
+    p.split = split_keys(S, N * Hk);
+    p.parts = (int)std::max<int64_t>(1, (S + p.split - 1) / p.split);
+    if (P > 0) {
+        p.psplit = split_keys(P, Hk * ((N * G + 63) / 64));
+        p.pparts = (int)((P + p.psplit - 1) / p.psplit);
+    }
+    p.direct = p.parts + p.pparts == 1;
+    if (!p.direct) {
+        const size_t rows = (size_t)(p.parts + p.pparts) * N * H;
+        p.off_lse = align_up(rows * D * sizeof(float), 256);
+        p.bytes = p.off_lse + align_up(rows * sizeof(float), 256);
+    }
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+sgla_status softmax_attention_fwd(const void *q, const void *k, const void *v, float scale, int causal, void *o,
+                                  float *lse, const int64_t *cu_seqlens_q, const int64_t *cu_seqlens_k, int64_t N,
+                                  int64_t Tq, int64_t Tk, int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype,
+                                  int *device_status, void *stream) {
+    AttnArgs a{};
+    int64_t q_tokens, k_tokens;
+    sgla_status s = check_seqs(a, cu_seqlens_q, cu_seqlens_k, N, Tq, Tk, H, Hk, D, dtype, scale, causal,
+                               device_status, q_tokens, k_tokens);
+    if (s != SGLA_OK) return s;
+    if ((q_tokens > 0 && (!q || !o)) || (k_tokens > 0 && (!k || !v))) return SGLA_ERR_INVALID_ARGUMENT;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!aligned(p, 16)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (!aligned(lse, 4)) return SGLA_ERR_INVALID_ARGUMENT;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = reset_status(device_status, st)) != SGLA_OK) return s;
+    if (q_tokens == 0) return SGLA_OK;
+    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+    ATTN_LAUNCH("softmax_attention_fwd", launch_attn_fwd_simt(a, st));
+    return SGLA_OK;
+}
+
+size_t softmax_attention_bwd_workspace_size(int64_t q_tokens, int64_t H) {
+    if (q_tokens < 0 || H < 1 || q_tokens >= kMaxTokens || H > 65535) return 0;
+    return align_up(std::max<size_t>(1, (size_t)q_tokens * H * sizeof(float)), 256);
+}
+
+sgla_status softmax_attention_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                  const void *dout, float scale, int causal, void *dq, void *dk, void *dv,
+                                  const int64_t *cu_seqlens_q, const int64_t *cu_seqlens_k, int64_t N, int64_t Tq,
+                                  int64_t Tk, int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype, int *device_status,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    AttnArgs a{};
+    int64_t q_tokens, k_tokens;
+    sgla_status s = check_seqs(a, cu_seqlens_q, cu_seqlens_k, N, Tq, Tk, H, Hk, D, dtype, scale, causal,
+                               device_status, q_tokens, k_tokens);
+    if (s != SGLA_OK) return s;
+    if (q_tokens > 0 && (!q || !o || !lse || !dout || !dq)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (k_tokens > 0 && (!k || !v || !dk || !dv)) return SGLA_ERR_INVALID_ARGUMENT;
+    for (const void *p : {q, k, v, o, dout, (const void *)dq, (const void *)dk, (const void *)dv})
+        if (!aligned(p, 16)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (!aligned(lse, 4) || !aligned(workspace, 256)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (!workspace || workspace_bytes < softmax_attention_bwd_workspace_size(q_tokens, H)) return SGLA_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = reset_status(device_status, st)) != SGLA_OK) return s;
+    a.q = q; a.k = k; a.v = v; a.dout = dout; a.lse_in = lse; a.delta = static_cast<float *>(workspace);
+    a.dq = dq; a.dk = dk; a.dv = dv;
+    if (q_tokens > 0) ATTN_LAUNCH("softmax_attention_delta", launch_attn_delta(a, o, st));
+    if (k_tokens > 0) ATTN_LAUNCH("softmax_attention_dkdv", launch_attn_bwd_dkdv_simt(a, st));
+    if (q_tokens > 0) ATTN_LAUNCH("softmax_attention_dq", launch_attn_bwd_dq_simt(a, st));
+    return SGLA_OK;
+}
+
+size_t softmax_attention_decode_workspace_size(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk, int64_t D,
+                                               sgla_dtype dtype) {
+    return decode_plan(N, S, P, H, Hk, D, dtype).bytes;
+}
+
+sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, const void *v_cache,
+                                          const int64_t *lengths, const void *prefix_k, const void *prefix_v,
+                                          float scale, void *o, int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk,
+                                          int64_t D, sgla_dtype dtype, int *device_status, void *workspace,
+                                          size_t workspace_bytes, void *stream) {
+    const DecodePlan p = decode_plan(N, S, P, H, Hk, D, dtype);
+    if (p.why != SGLA_OK) return p.why;
+    if (!aligned(device_status, 4) || !aligned(lengths, 8)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (N > 0 && (!q || !o || !lengths || (S > 0 && (!k_cache || !v_cache)) || (P > 0 && (!prefix_k || !prefix_v))))
+        return SGLA_ERR_INVALID_ARGUMENT;
+    for (const void *x : {q, k_cache, v_cache, prefix_k, prefix_v, (const void *)o})
+        if (!aligned(x, 16)) return SGLA_ERR_INVALID_ARGUMENT;
+    if (p.bytes > 0) {
+        if (!workspace || workspace_bytes < p.bytes) return SGLA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return SGLA_ERR_INVALID_ARGUMENT;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const sgla_status s = reset_status(device_status, st);
+    if (s != SGLA_OK || N == 0) return s;
+    AttnArgs a{};
+    a.q = q; a.k = k_cache; a.v = v_cache; a.o = o;
+    a.scale = pick_scale(scale, D);
+    a.bf16 = dtype == SGLA_BF16;
+    a.N = N;
+    a.sq.T = 1;
+    a.sk.T = S; a.sk.len = lengths;
+    a.H = (int)H; a.Hk = (int)Hk; a.G = (int)(H / Hk); a.D = (int)D;
+    a.status = device_status;
+    a.split = p.split; a.nsplit = p.parts;
+    a.part_rows = N * H;
+    float *part_o = static_cast<float *>(workspace);
+    float *part_lse = p.direct ? nullptr : reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_lse);
+    if (!p.direct) {
+        a.part_o = part_o;
+        a.part_lse = part_lse;
+    }
+    ATTN_LAUNCH("softmax_attention_decode", launch_attn_fwd_simt(a, st));
+    if (p.direct) return SGLA_OK;
+    if (P > 0) {  // every query token against the prefix, as one sequence
+        a.k = prefix_k; a.v = prefix_v;
+        a.N = 1;
+        a.sq.T = N;
+        a.sk.T = P; a.sk.len = nullptr;
+        a.split = p.psplit; a.nsplit = p.pparts;
+        a.part_o = part_o + (int64_t)p.parts * N * H * D;
+        a.part_lse = part_lse + (int64_t)p.parts * N * H;
+        ATTN_LAUNCH("softmax_attention_prefix", launch_attn_fwd_simt(a, st));
+    }
+    ATTN_LAUNCH("softmax_attention_join",
+                launch_attn_join(part_o, part_lse, o, N * H, p.parts + p.pparts, (int)D, a.bf16, st));
+    return SGLA_OK;
+}
+
+}  // extern "C"

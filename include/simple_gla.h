@@ -499,6 +499,87 @@ SGLA_API sgla_status simple_gla_normalized_decode_step(const void *q, const void
                                               void *stream);
 
 /*
+ * Softmax attention over the same head layout: the token mixer of the layers that a
+ * conversion to a hybrid model keeps ("relinear -- convert pretrained transformers to
+ * linear/hybrid-attention models"), with its gradients and its one-token step.
+ *   s_ij = scale q_i . k_j for the keys j that query i sees, p_i = softmax(s_i),
+ *   o_i = sum_j p_ij v_j,  lse_i = log sum_j exp s_ij  (natural log).
+ * Query head h reads key head h / (H / Hk).  With causal != 0 query i of a sequence of tq
+ * queries and tk keys sees the keys j <= i + tk - tq.  A query that sees no key has o = 0,
+ * lse = -inf and adds nothing to any gradient.
+ *   q, o, dout, dq [q tokens, H, D]; k, v, dk, dv [k tokens, Hk, D] in dtype; lse
+ *   [q tokens, H] fp32 (forward: NULL when not wanted; backward: the forward's).
+ *   cu_seqlens_q == cu_seqlens_k == NULL: N sequences of Tq queries and Tk keys.
+ *   Both given: DEVICE pointers to N+1 int64 (N >= 1; they may be one array), Tq and Tk
+ *       the token counts in all.  A sequence whose bounds are not 0 <= start <= end <= T
+ *       on both sides is skipped (its outputs are not written) and *device_status, when
+ *       given, is set to SGLA_DEVICE_BAD_CU_SEQLENS.  Tokens behind the last sequence
+ *       belong to none: their outputs are zeros (lse -inf).
+ *   device_status: optional DEVICE int, reset to SGLA_DEVICE_OK by these calls.
+ *   scale as simple_gla_fwd (NaN or <= 0 selects 1/sqrt(D)).
+ * Only what a query sees is meant to be finite for its output to be; a value that is not
+ * finite in a key or value later in the same tile of 128 keys can reach a causal query as
+ * NaN (0 times it).  Keys behind a sequence's end are never read into a result.
+ * Supported sizes: D <= 128 and a multiple of 8, H a multiple of Hk, H / Hk <= 128,
+ * H <= 65535, fewer than 2^31 tokens.  Tensor pointers 16-byte aligned.
+ * Results do not depend on the order in which thread blocks run (no atomics).
+ *
+ * softmax_attention_bwd: dq, dk, dv for the loss sum(o dout), with o and lse those of
+ * the forward on the same inputs; the probabilities are recomputed from lse.  workspace:
+ * softmax_attention_bwd_workspace_size(q tokens, H) bytes, 256-byte aligned.
+ */
+SGLA_API sgla_status softmax_attention_fwd(const void *q, const void *k, const void *v, float scale, int causal,
+                                           void *o, float *lse, const int64_t *cu_seqlens_q,
+                                           const int64_t *cu_seqlens_k, int64_t N, int64_t Tq, int64_t Tk, int64_t H,
+                                           int64_t Hk, int64_t D, sgla_dtype dtype, int *device_status, void *stream);
+SGLA_API size_t softmax_attention_bwd_workspace_size(int64_t q_tokens, int64_t H);
+SGLA_API sgla_status softmax_attention_bwd(const void *q, const void *k, const void *v, const void *o,
+                                           const float *lse, const void *dout, float scale, int causal, void *dq,
+                                           void *dk, void *dv, const int64_t *cu_seqlens_q,
+                                           const int64_t *cu_seqlens_k, int64_t N, int64_t Tq, int64_t Tk, int64_t H,
+                                           int64_t Hk, int64_t D, sgla_dtype dtype, int *device_status,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of softmax attention for N sequences: o[n] = attention of q[n] over the first
+ * lengths[n] keys of its cache and, when P > 0, over P keys that every sequence has in
+ * front of its own (a prompt shared by the batch: read once for all of them).
+ *   q, o [N,H,D]; k_cache, v_cache [N,S,Hk,D]; prefix_k, prefix_v [P,Hk,D] (NULL when
+ *   P == 0), all in dtype; lengths DEVICE int64 [N], 0 <= lengths[n] <= S (the new token's
+ *   key among them, if it is to be seen).  What lies behind lengths[n] is not read into
+ *   the result.  A length outside that range counts as 0 and sets *device_status (optional
+ *   DEVICE int, reset by the call) to SGLA_DEVICE_BAD_CU_SEQLENS.  No key at all: o = 0.
+ * Heads, D, scale, alignment as softmax_attention_fwd; N * max(S, H) < 2^31.  workspace:
+ * softmax_attention_decode_workspace_size() bytes (0: none needed), 256-byte aligned.
+ */
+SGLA_API size_t softmax_attention_decode_workspace_size(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk,
+                                                        int64_t D, sgla_dtype dtype);
+SGLA_API sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, const void *v_cache,
+                                                   const int64_t *lengths, const void *prefix_k,
+                                                   const void *prefix_v, float scale, void *o, int64_t N, int64_t S,
+                                                   int64_t P, int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype,
+                                                   int *device_status, void *workspace, size_t workspace_bytes,
+                                                   void *stream);
+
+/*
+ * Rotary positions with one or more axes for q and k, in front of either token mixer
+ * ("relinear": the layer's _qk_transform): pair i of the R / 2 rotated pairs of every head
+ * turns by theta = positions[t, axis_of_pair[i]] * inv_freq[i],
+ *   (x, y) -> (x cos theta - y sin theta, x sin theta + y cos theta),
+ * pairs (i, i + R/2), or (2i, 2i + 1) with interleaved != 0; columns R .. D-1 are copied.
+ * inverse != 0 rotates by -theta: the gradient of the call, and its undoing.
+ *   q, q_out [tokens,H,D], k, k_out [tokens,Hk,D] in dtype (H or Hk may be 0, its pointers
+ *   then NULL); positions DEVICE int64 [tokens,A]; inv_freq DEVICE fp32 [R/2];
+ *   axis_of_pair HOST uint8 [R/2], each < A.  Angles are formed in 64 bits.
+ * Supported sizes: D even, D <= 4096, R even, R <= min(D, 512), 1 <= A <= 255,
+ * H + Hk <= 65535, fewer than 2^31 tokens.  Tensor pointers 16-byte aligned.  No workspace.
+ */
+SGLA_API sgla_status multi_axis_rotary(const void *q, const void *k, const int64_t *positions, const float *inv_freq,
+                                       const uint8_t *axis_of_pair, void *q_out, void *k_out, int64_t tokens,
+                                       int64_t H, int64_t Hk, int64_t D, int64_t R, int64_t A, int interleaved,
+                                       int inverse, sgla_dtype dtype, void *stream);
+
+/*
  * Self-test of the library's failure detection (no counterpart on the pages).  Every
  * wait of the tensor-core pipelines on an mbarrier is bounded: after 2 s of wall time
  * the waiting thread gives up, raises its CTA's abort flag (on which the CTA's other
