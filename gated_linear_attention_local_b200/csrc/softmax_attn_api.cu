@@ -66,6 +66,10 @@ sgla_status check_seqs(AttnArgs &a, const int64_t *cu_q, const int64_t *cu_k, in
     return SGLA_OK;
 }
 
+cudaError_t launch_fwd(const AttnArgs &a, cudaStream_t st) {
+    return a.bf16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, st);
+}
+
 // The one-token step: keys are split so that the GPU is filled, the prefix of all sequences
 // is one sequence of N query tokens, and the parts of a row are joined at the end.
 struct DecodePlan {
@@ -128,7 +132,7 @@ sgla_status softmax_attention_fwd(const void *q, const void *k, const void *v, f
     if ((s = reset_status(device_status, st)) != SGLA_OK) return s;
     if (q_tokens == 0) return SGLA_OK;
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
-    ATTN_LAUNCH("softmax_attention_fwd", launch_attn_fwd_simt(a, st));
+    ATTN_LAUNCH("softmax_attention_fwd", launch_fwd(a, st));
     return SGLA_OK;
 }
 
@@ -204,7 +208,7 @@ sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, co
         a.part_o = part_o;
         a.part_lse = part_lse;
     }
-    ATTN_LAUNCH("softmax_attention_decode", launch_attn_fwd_simt(a, st));
+    ATTN_LAUNCH("softmax_attention_decode", launch_fwd(a, st));
     if (p.direct) return SGLA_OK;
     if (P > 0) {  // every query token against the prefix, as one sequence
         a.k = prefix_k; a.v = prefix_v;
@@ -214,7 +218,7 @@ sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, co
         a.split = p.psplit; a.nsplit = p.pparts;
         a.part_o = part_o + (int64_t)p.parts * N * H * D;
         a.part_lse = part_lse + (int64_t)p.parts * N * H;
-        ATTN_LAUNCH("softmax_attention_prefix", launch_attn_fwd_simt(a, st));
+        ATTN_LAUNCH("softmax_attention_prefix", launch_fwd(a, st));
     }
     ATTN_LAUNCH("softmax_attention_join",
                 launch_attn_join(part_o, part_lse, o, N * H, p.parts + p.pparts, (int)D, a.bf16, st));
