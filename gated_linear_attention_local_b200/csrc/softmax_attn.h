@@ -56,6 +56,8 @@ cudaError_t launch_attn_bwd_dkdv_simt(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_bwd_dq_simt(const AttnArgs &a, cudaStream_t st);
 // tensor cores, bf16
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dkdv_tc(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dq_tc(const AttnArgs &a, cudaStream_t st);
 // delta_i = sum_d do_id o_id, one value a row
 cudaError_t launch_attn_delta(const AttnArgs &a, const void *o, cudaStream_t st);
 

@@ -162,8 +162,12 @@ sgla_status softmax_attention_bwd(const void *q, const void *k, const void *v, c
     a.q = q; a.k = k; a.v = v; a.dout = dout; a.lse_in = lse; a.delta = static_cast<float *>(workspace);
     a.dq = dq; a.dk = dk; a.dv = dv;
     if (q_tokens > 0) ATTN_LAUNCH("softmax_attention_delta", launch_attn_delta(a, o, st));
-    if (k_tokens > 0) ATTN_LAUNCH("softmax_attention_dkdv", launch_attn_bwd_dkdv_simt(a, st));
-    if (q_tokens > 0) ATTN_LAUNCH("softmax_attention_dq", launch_attn_bwd_dq_simt(a, st));
+    // dq first: it sharpens delta for rows with few keys
+    if (q_tokens > 0)
+        ATTN_LAUNCH("softmax_attention_dq", a.bf16 ? launch_attn_bwd_dq_tc(a, st) : launch_attn_bwd_dq_simt(a, st));
+    if (k_tokens > 0)
+        ATTN_LAUNCH("softmax_attention_dkdv",
+                    a.bf16 ? launch_attn_bwd_dkdv_tc(a, st) : launch_attn_bwd_dkdv_simt(a, st));
     return SGLA_OK;
 }
 
