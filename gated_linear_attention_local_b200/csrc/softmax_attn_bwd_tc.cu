@@ -90,6 +90,7 @@ __device__ __forceinline__ void zero_rows(unsigned char *pair, int from, int lan
 
 __device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
     float x[32], y[32];
+    __syncwarp();
     tmem_ld32(taddr, x);
     tmem_ld32(taddr + 32, y);
     tmem_wait_ld();
@@ -101,6 +102,7 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
 }
 
 __device__ __forceinline__ void st64_bf16(uint32_t taddr, const float (&v)[64]) {
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -113,6 +115,7 @@ __device__ __forceinline__ void st64_bf16(uint32_t taddr, const float (&v)[64]) 
 
 // Columns [0, D) of this thread's accumulator row times f, as bf16 to dst (zeros with !any).
 __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, __nv_bfloat16 *dst, int D, float f) {
+    __syncwarp();
     for (int c = 0; c < D; c += 32) {
         float o[32];
         if (any) {
@@ -121,13 +124,14 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, _
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f : 0.f;
-        if (!mine) continue;
+        if (mine)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + 8 * e < D)
-                *reinterpret_cast<uint4 *>(dst + c + 8 * e) =
-                    make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                               pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+            for (int e = 0; e < 4; ++e)
+                if (c + 8 * e < D)
+                    *reinterpret_cast<uint4 *>(dst + c + 8 * e) =
+                        make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                   pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+        __syncwarp();  // the next tensor memory read is the whole warp's
     }
 }
 
@@ -354,6 +358,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             atomicExch(a.status, kDevTimeout);
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
@@ -504,7 +509,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     if (c < lim) x = fmaf(p[c], dp[c], x);
                 if (lim > 0 && lim <= kSub) {
                     delta = x;
-                    a.delta[row] = x;
+                    if (mine) a.delta[row] = x;
                 }
             }
 #pragma unroll
@@ -528,6 +533,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             atomicExch(a.status, kDevTimeout);
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {

@@ -1,24 +1,36 @@
 // Softmax attention forward on the tensor cores (tcgen05 / TMEM / TMA), bf16 operands.
 //
-// One CTA takes two tiles of 128 packed rows (row = token * G + g of one key head, R = 128 / G
-// tokens a tile) and walks the keys in tiles of 128.  For each tile w of rows and key tile j
+// A work item is two tiles of 128 packed rows (row = token * G + g of one key head, R = 128 / G
+// tokens a tile) against the keys its rows see, in tiles of 128.  For row tile w, key tile j
 //   S_w = Q_w K_j^T            (128 x 128, fp32 in tensor memory)
 //   p   = 2^(sc S - m)         one thread a row: maximum and sum need no shuffles
 //   O_w += P_w V_j             P_w in bf16 in tensor memory, over S_w's columns
 // The two row tiles alternate: while one's 128 threads form p, the tensor cores run the other's
 // products.  The tensor pipe executes in issue order, so S_w(j+1) may follow P_w(j) V_j at
-// once although it overwrites P_w(j).
+// once although it overwrites P_w(j).  P_w V_j starts when the first 96 of its 128 keys are
+// written.
+//
+// One CTA per SM takes items in turn (heaviest first); a scheduler warp finds the sequence of
+// the next item and hands out its description while the current one is in work, and the copies
+// and first products of an item run under the epilogue of the one before.
 //
 // The maximum m of a row is only moved (and O, l rescaled, in tensor memory, by the row's own
 // thread) when it has grown by more than 2^8: until then p <= 2^8, which fp32 sums and the
 // bf16 range (the rounding is relative) carry without loss.
+//
+// Exponentials: 128 x 128 of them take the special-function unit as long as the two products
+// take the tensor cores (1024 cycles), so a quarter goes to the FMA pipe instead: with
+// n = round(x), f = x - n, 2^x = 2^n p3(f), p3 the degree-3 polynomial of least largest relative
+// error on [-1/2, 1/2] (Remez exchange; 7.5e-5, a fiftieth of the rounding of p to bf16 that
+// follows).  A NaN among a row's visible scores makes its maximum and so all its p NaN.
 //
 // p is rounded to bf16 for the product with V (relative 2^-8, averaged over the keys); its sum
 // l, m, S and O are fp32.
 //
 // Tensor memory (512 columns): S0, S1 [0, 256), O0, O1 [256, 512).
 // Shared memory (DP = 128): Q 64 KB, rings of two K and two V tiles 128 KB.
-// Warps: 0-3 rows of tile 0, 4-7 rows of tile 1, 8 TMA, 9 MMA (10, 11 fill its warpgroup).
+// Warps: 0-3 rows of tile 0, 4-7 rows of tile 1, 8 TMA, 9 MMA, 10 scheduler (11 fills up).
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -39,64 +51,106 @@ constexpr int kFwdThreads = 384;
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
 constexpr int kRowRegs = 208, kOtherRegs = 80;
 constexpr int kTile = 128;
+constexpr int kSms = 148;  // one persistent CTA each
+constexpr int kItems = 2;  // item descriptions in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 units the maximum may lag behind
+
+// What the roles need to know of a work item; every count fits 32 bits.
+struct Item {
+    int nt[2];     // key tiles of each row tile; nt[0] < 0: no more items
+    int q_tok;     // first token of row tile 0
+    int q_left;    // tokens of the sequence from there on
+    int k_tok;     // first key of this split
+    int keys;      // keys of this split
+    int k_left;    // keys of the sequence from k_tok on
+    int shift;     // causal: token x of the item sees keys < x + 1 + shift of this split
+    int hk, z;     // key head, split
+};
 
 template <int DP>
 struct FwdCfg {
     static constexpr int NG = DP / 64;               // 64-column groups of a tile
     static constexpr uint32_t T = NG * kRegion;      // one tile, bytes
     static constexpr uint32_t Q0 = 0, K0 = 2 * T, V0 = 4 * T;
-    static constexpr uint32_t BARS = 6 * T, MISC = BARS + 20 * 8;
+    static constexpr uint32_t BARS = 6 * T, MISC = BARS + 32 * 8, ITEMS = MISC + 16;
     // at least half of an SM's shared memory: the CTA takes all of its tensor memory
-    static constexpr size_t SMEM = MISC + 16 + 1024 > 120 * 1024 ? MISC + 16 + 1024 : 120 * 1024;
+    static constexpr size_t NEED = ITEMS + kItems * sizeof(Item) + 1024;
+    static constexpr size_t SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t COL_O = 256;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// (2^x, 2^y) on the FMA pipe for x, y <= 8, finite: see the head of this file.  Below -126 the
+// result is 2^-126.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are round(x)
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    const float2 t = __fadd2_rn(x, magic);
+    const float2 f = __fadd2_rn(x, __fadd2_rn(magic, make_float2(-t.x, -t.y)));
+    float2 p = __ffma2_rn(f, make_float2(0.0551716685f, 0.0551716685f), make_float2(0.2426111251f, 0.2426111251f));
+    p = __ffma2_rn(p, f, make_float2(0.6932609677f, 0.6932609677f));
+    p = __ffma2_rn(p, f, make_float2(0.9999280572f, 0.9999280572f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
+// p of the scores s[0..32) of a row, as bf16 to 16 columns at taddr; their sum onto sum.
+template <bool MASKED>
+__device__ __forceinline__ void probabilities(const float (&s)[32], float sc, float ms, uint32_t taddr, float2 (&sum)[2]) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), make_float2(sc, sc), make_float2(-ms, -ms));
+        if (!MASKED && (e & 3) == 3) {
+            x = exp2_fma(x);
+        } else {
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+        }
+        sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+        p[e] = pack_bf16(x.x, x.y);
+    }
+    tmem_st16(taddr, p);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
+                   const __grid_constant__ CUtensorMap tv, AttnArgs a, int R, int slots) {
     using C = FwdCfg<DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = align1024(smem_raw);
-    AttnTile t;
-    const int hk = blockIdx.x % a.Hk;
-    // heaviest first: a causal sequence's last rows see the most keys
-    int64_t slot = gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk;
-    if (!a.sq.cu) {
-        const int64_t per = gridDim.x / a.Hk / a.N;
-        slot = (slot % a.N) * per + slot / a.N;
-    }
-    if (!attn_locate(a, true, slot, 1, 2 * R, t)) return;
-    const int64_t kb = (int64_t)blockIdx.y * a.split, ke = min64(t.tk, kb + a.split);
-    // key tiles of each row tile: up to the last key its last row sees
-    int nt[2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const int64_t last = min64(t.row0 + (w + 1) * R, t.tq) - 1;  // last token
-        int64_t lim = a.causal ? min64(ke, last + 1 + t.tk - t.tq) : ke;
-        if (t.row0 + w * R >= t.tq) lim = 0;
-        nt[w] = lim > kb ? (int)((lim - kb + kTile - 1) / kTile) : 0;
-    }
-    const int n = max(nt[0], nt[1]);
-
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::BARS);
-    uint64_t *full_q = bars, *full_k = bars + 2, *full_v = bars + 4;   // [2]
-    uint64_t *empty_k = bars + 6, *empty_v = bars + 8;                 // [2]
-    uint64_t *b_s = bars + 10, *b_p = bars + 12, *b_o = bars + 14;     // [2] per row tile
-    uint64_t *b_drain = bars + 16;
+    uint64_t *full_q = bars, *empty_q = bars + 2;                      // [2] per row tile
+    uint64_t *full_k = bars + 4, *full_v = bars + 6;                   // [2] stages
+    uint64_t *empty_k = bars + 8, *empty_v = bars + 10;                // [2]
+    uint64_t *b_s = bars + 12, *b_o = bars + 14;                       // [2] per row tile: S, O complete
+    uint64_t *b_pa = bars + 16, *b_pb = bars + 18;                     // [2] first 96, last 32 keys of P written
+    uint64_t *full_i = bars + 20, *empty_i = bars + 20 + kItems;       // [kItems] descriptions
+    uint64_t *b_drain = bars + 20 + 2 * kItems;
+    Item *items = reinterpret_cast<Item *>(sm + C::ITEMS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int b = 0; b < 12; ++b) mbar_init(&bars[b], 1);
-        mbar_init(&b_p[0], 128);
-        mbar_init(&b_p[1], 128);
-        mbar_init(&b_o[0], 1);
-        mbar_init(&b_o[1], 1);
+        for (int b = 0; b < 16; ++b) mbar_init(&bars[b], 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&b_pa[b], 128);
+            mbar_init(&b_pb[b], 128);
+        }
+        for (int b = 0; b < kItems; ++b) {
+            mbar_init(&full_i[b], 1);
+            mbar_init(&empty_i[b], 10);  // one arrival a consuming warp
+        }
         mbar_init(b_drain, 1);
         *abort_flag = 0;
         mbar_fence_init();
@@ -109,39 +163,104 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The next item's description, for every lane of a warp; false when there is none.
+    auto next_item = [&](int &count, Item &it) -> bool {
+        const int st = count % kItems;
+        if (!mbar_wait(&full_i[st], (count / kItems) & 1, abort_flag)) return false;
+        it = items[st];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_i[st]);
+        ++count;
+        return it.nt[0] >= 0;
+    };
 
-    if (warp == 8) {
+    if (warp == 10) {
+        // ---------------------------------------------------------------- scheduler
+        setmaxnreg_dec<kOtherRegs>();
+        const int per_z = slots * a.Hk, total = per_z * a.nsplit;
+        int count = 0;
+        bool ok = true;
+        auto publish = [&](const Item &it) {
+            const int st = count % kItems;
+            if (count >= kItems) ok = mbar_wait(&empty_i[st], ((count / kItems) - 1) & 1, abort_flag);
+            if (ok && lane == 0) {
+                items[st] = it;
+                mbar_arrive(&full_i[st]);
+            }
+            __syncwarp();
+            ++count;
+        };
+        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+            Item it;
+            it.z = u / per_z;
+            const int rest = u - it.z * per_z;
+            it.hk = rest % a.Hk;
+            // heaviest first: a causal sequence's last rows see the most keys
+            int64_t slot = slots - 1 - rest / a.Hk;
+            if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+            AttnTile t;
+            if (!attn_locate(a, true, slot, 1, 2 * R, t)) continue;
+            const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
+            it.keys = (int)(ke > kb ? ke - kb : 0);
+            it.q_tok = (int)(t.q0 + t.row0);
+            it.q_left = (int)(t.tq - t.row0);
+            it.k_tok = (int)(t.k0 + kb);
+            it.k_left = (int)(t.tk - kb);
+            it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX / 2), -(int64_t)INT_MAX / 2);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
+                const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
+                it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
+            }
+            publish(it);
+        }
+        Item end{};
+        end.nt[0] = -1;
+        if (ok) publish(end);
+    } else if (warp == 8) {
         // ---------------------------------------------------------------- TMA producer
         setmaxnreg_dec<kOtherRegs>();
-        if (lane == 0) {
-            const uint32_t qbytes = (uint32_t)(R * a.G) * 128u * C::NG;
-            for (int w = 0; w < 2; ++w) {
-                if (nt[w] == 0) continue;
-                mbar_arrive_expect_tx(&full_q[w], qbytes);
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, hk * a.G,
-                                (int)(t.q0 + t.row0 + w * R));
+        const uint32_t qbytes = (uint32_t)(R * a.G) * 128u * C::NG;
+        Item it;
+        int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
+        bool ok = true;
+        while (ok && next_item(ni, it)) {
+            if (lane == 0) {
+                for (int w = 0; ok && w < 2; ++w) {
+                    if (it.nt[w] == 0) continue;
+                    if (nq[w] > 0 && !(ok = mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag))) break;
+                    mbar_arrive_expect_tx(&full_q[w], qbytes);
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, it.hk * a.G,
+                                    it.q_tok + w * R);
+                    ++nq[w];
+                }
+                const int n = max(it.nt[0], it.nt[1]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int st = kv & 1;
+                    const uint32_t ph = ((kv >> 1) - 1) & 1;
+                    if (kv >= 2 && !(ok = mbar_wait_idle(&empty_k[st], ph, abort_flag))) break;
+                    mbar_arrive_expect_tx(&full_k[st], C::T);
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, it.hk,
+                                    it.k_tok + j * kTile);
+                    ++kv;
+                    if (nv >= 2 && !(ok = mbar_wait_idle(&empty_v[st], ph, abort_flag))) break;
+                    mbar_arrive_expect_tx(&full_v[st], C::T);
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, it.hk,
+                                    it.k_tok + j * kTile);
+                    ++nv;
+                }
             }
-            int j = 0;
-            for (; j < n; ++j) {
-                const int st = j & 1;
-                const uint32_t ph = ((j >> 1) - 1) & 1;
-                const int tok = (int)(t.k0 + kb + (int64_t)j * kTile);
-                if (j >= 2 && !mbar_wait_idle(&empty_k[st], ph, abort_flag)) break;
-                mbar_arrive_expect_tx(&full_k[st], C::T);
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, hk, tok);
-                if (j >= 2 && !mbar_wait_idle(&empty_v[st], ph, abort_flag)) break;
-                mbar_arrive_expect_tx(&full_v[st], C::T);
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, hk, tok);
-            }
-            if (*abort_flag) {  // let the copies in flight land before the CTA exits
-                for (int w = 0; w < 2; ++w)
-                    if (nt[w]) mbar_drain(&full_q[w], 0);
-                for (int i = max(0, j - 2); i <= min(j, n - 1); ++i) mbar_drain(&full_k[i & 1], (i >> 1) & 1);
-                for (int i = max(0, j - 2); i < j; ++i) mbar_drain(&full_v[i & 1], (i >> 1) & 1);
-            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA exits
+            for (int w = 0; w < 2; ++w)
+                if (nq[w] > 0) mbar_drain(&full_q[w], (nq[w] - 1) & 1);
+            for (int i = max(0, kv - 2); i < kv; ++i) mbar_drain(&full_k[i & 1], (i >> 1) & 1);
+            for (int i = max(0, nv - 2); i < nv; ++i) mbar_drain(&full_v[i & 1], (i >> 1) & 1);
         }
     } else if (warp == 9) {
         // ---------------------------------------------------------------- MMA issuer
@@ -150,69 +269,94 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int nk = (a.D + 15) / 16;  // 16-column steps of a head (zeros past D)
         const uint32_t idO = idesc_bf16_f32(128, 16 * nk, false, true);
         const uint32_t sbase = smem_u32(sm);
+        const uint64_t qd = kdesc(sbase + C::Q0), kd = kdesc(sbase + C::K0);
+        const uint64_t vd = sdesc(sbase + C::V0, kRegion, 1024, 2);
         auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-        auto issue_S = [&](int w, int j) {
-            if (lane == 0) {
-                const uint32_t qa = sbase + C::Q0 + w * C::T, ka = sbase + C::K0 + (j & 1) * C::T;
-                for (int kk = 0; kk < nk; ++kk) {
-                    const uint32_t off = (kk >> 2) * kRegion + (kk & 3) * 32;
-                    mma_bf16(tmem + w * 128, kdesc(qa + off), kdesc(ka + off), idS, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(&b_s[w]);
-            }
-            __syncwarp();
-        };
+        Item it;
+        int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
         bool ok = true;
-        for (int j = -1; ok && j < n; ++j) {
-            const int st = j & 1;
-            bool vready = false, kready = false;
-            for (int w = 0; ok && w < 2; ++w) {
-                if (j >= 0 && j < nt[w]) {
-                    if (!vready) {
-                        if (!(ok = wait(&full_v[st], (j >> 1) & 1))) break;
-                        vready = true;
-                        const int64_t valid = t.tk - (kb + (int64_t)j * kTile);
-                        if (valid < kTile) {
-                            // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
-                            for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
-                                const int r = (i >> 3) & (kTile - 1);
-                                if (r >= valid)
-                                    *reinterpret_cast<uint4 *>(sm + C::V0 + st * C::T + (i >> 10) * kRegion + r * 128 +
-                                                               (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if (!(ok = wait(&b_p[w], j & 1))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t va = sbase + C::V0 + st * C::T;
+        while (ok && next_item(ni, it)) {
+            // the same in every lane; the reduction leaves them in uniform registers, from which
+            // the products' descriptors are formed without a move per operand
+            const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
+            const int n = max(nt[0], nt[1]);
+            for (int j = -1; ok && j < n; ++j) {
+                const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
+                bool vready = false, kready = false;
 #pragma unroll
-                        for (int jj = 0; jj < kTile / 16; ++jj)
-                            mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
-                                            sdesc(va + jj * 2048, kRegion, 1024, 2), idO, (j > 0 || jj > 0) ? 1u : 0u);
-                        if (j == nt[w] - 1) mma_commit(&b_o[w]);
+                for (int w = 0; w < 2; ++w) {
+                    if (!ok) break;
+                    if (j >= 0 && j < nt[w]) {
+                        const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T);
+                        if (!vready) {
+                            if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
+                            vready = true;
+                            const int valid = it.k_left - j * kTile;
+                            if (valid < kTile) {
+                                // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
+                                for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
+                                    const int r = (i >> 3) & (kTile - 1);
+                                    if (r >= valid)
+                                        *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion +
+                                                                   r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        if (!(ok = wait(&b_pa[w], np[w] & 1))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int jj = 0; jj < 6; ++jj)
+                                mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
+                                                desc_at(v0, jj * 2048), idO, (j > 0 || jj > 0) ? 1u : 0u);
+                        }
+                        __syncwarp();
+                        if (!(ok = wait(&b_pb[w], np[w] & 1))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int jj = 6; jj < 8; ++jj)
+                                mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
+                                                desc_at(v0, jj * 2048), idO, 1u);
+                            if (j == nt[w] - 1) mma_commit(&b_o[w]);
+                        }
+                        ++np[w];
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (j + 1 < nt[w]) {
-                    if (j < 0 && !(ok = wait(&full_q[w], 0))) break;
-                    if (!kready) {
-                        if (!(ok = wait(&full_k[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
-                        kready = true;
+                    if (j + 1 < nt[w]) {
+                        if (j < 0) {
+                            if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
+                            ++nq[w];
+                        }
+                        if (!kready) {
+                            if (!(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
+                            kready = true;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t q1 = desc_at(qd, w * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
+#pragma unroll
+                            for (int kk = 0; kk < DP / 16; ++kk)
+                                if (kk < nk)
+                                    mma_bf16(tmem + w * 128, desc_at(q1, (kk >> 2) * kRegion + (kk & 3) * 32),
+                                             desc_at(k1, (kk >> 2) * kRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+                            mma_commit(&b_s[w]);
+                            if (j + 1 == nt[w] - 1) mma_commit(&empty_q[w]);
+                        }
+                        __syncwarp();
                     }
-                    tc_fence_after();
-                    issue_S(w, j + 1);
                 }
+                if (ok && elect_one()) {
+                    if (j >= 0) mma_commit(&empty_v[c0 & 1]);
+                    if (j + 1 < n) mma_commit(&empty_k[c1 & 1]);
+                }
+                __syncwarp();
             }
-            if (ok && lane == 0) {
-                if (j >= 0) mma_commit(&empty_v[st]);
-                if (j + 1 < n) mma_commit(&empty_k[(j + 1) & 1]);
-            }
-            __syncwarp();
+            kv += n;
         }
-        if (lane == 0) {
+        if (elect_one()) {
             mma_commit(b_drain);
             mbar_drain(b_drain, 0);
         }
@@ -222,77 +366,92 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int w = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t cS = tmem + w * 128 + lanes, cO = tmem + C::COL_O + w * 128 + lanes;
-        const int tr = r / a.G;
-        const int64_t tok = t.row0 + w * R + tr;
-        const bool mine = tr < R && tok < t.tq;
-        int64_t lim64 = mine ? (a.causal ? min64(ke, tok + 1 + t.tk - t.tq) : ke) : 0;
-        const int lim = (int)(lim64 > kb ? lim64 - kb : 0);  // keys of this split that the row sees
+        const int tr = r / a.G, x = w * R + tr;  // the row's token of the item
         const float sc = a.scale * kLog2e;
-        float m = -INFINITY, l = 0.f;  // m in units of S
+        Item it;
+        int ni = 0, ns = 0, no = 0;
         bool ok = true;
-        for (int j = 0; j < nt[w]; ++j) {
-            if (!(ok = mbar_wait(&b_s[w], j & 1, abort_flag))) break;
-            tc_fence_after();
-            float s[4][32];
+        while (ok && next_item(ni, it)) {
+            const bool mine = tr < R && x < it.q_left;
+            const int n = it.nt[w];
+            const int lim = mine ? (a.causal ? min(it.keys, x + 1 + it.shift) : it.keys) : 0;  // keys the row sees
+            float m = -INFINITY, l = 0.f;  // m in units of S
+            for (int j = 0; j < n; ++j, ++ns) {
+                if (!(ok = mbar_wait(&b_s[w], ns & 1, abort_flag))) break;
+                __syncwarp();
+                tc_fence_after();
+                float s[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(cS + 32 * c, s[c]);
-            tmem_wait_ld();
-            const int left = lim - j * kTile;
-            if (__any_sync(0xffffffffu, left < kTile)) {
+                for (int c = 0; c < 4; ++c) tmem_ld32(cS + 32 * c, s[c]);
+                tmem_wait_ld();
+                const int left = lim - j * kTile;
+                const bool masked = __any_sync(0xffffffffu, left < kTile);
+                if (masked) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e >= left) s[c][e] = -INFINITY;
-            }
-            float top = -INFINITY;
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= left) s[c][e] = -INFINITY;
+                }
+                float t4[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) t4[c] = max3_nan(s[c][0], s[c][1], s[c][2]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, s[c][e]);
-            // move the maximum when it has grown by more than kGrow (or there was none)
-            float f = 1.f;
-            if ((top - m) * sc > kGrow) {
-                f = fast_exp2((m - top) * sc);  // 0 from m = -inf
-                m = top;
-            }
-            if (__any_sync(0xffffffffu, f != 1.f)) {
-                l *= f;
-                if (j > 0) {
-                    for (int c = 0; c < a.D; c += 32) {
-                        float o[32];
-                        tmem_ld32(cO + c, o);
-                        tmem_wait_ld();
+                for (int e = 3; e + 1 < 32; e += 2)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st32(cO + c, o);
+                    for (int c = 0; c < 4; ++c) t4[c] = max3_nan(t4[c], s[c][e], s[c][e + 1]);
+                const float top = max3_nan(max3_nan(t4[0], t4[1], s[0][31]), max3_nan(t4[2], t4[3], s[1][31]),
+                                           max3_nan(s[2][31], s[3][31], s[3][31]));
+                // move the maximum when it has grown by more than kGrow, there was none, or it is NaN
+                float f = 1.f;
+                if (!((top - m) * sc <= kGrow) && top != -INFINITY) {
+                    f = fast_exp2((m - top) * sc);  // 0 from m = -inf
+                    m = top;
+                }
+                __syncwarp();
+                if (__any_sync(0xffffffffu, f != 1.f)) {
+                    l *= f;
+                    if (j > 0) {
+                        for (int c = 0; c < a.D; c += 16) {
+                            float o[16];
+                            tmem_ld16f(cO + c, o);
+                            tmem_wait_ld();
+                            uint32_t u[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                            tmem_st16(cO + c, u);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
                 }
+                const float ms = m == -INFINITY ? 0.f : m * sc;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                auto part = [&](int c) {
+                    if (masked) probabilities<true>(s[c], sc, ms, cS + 16 * c, sum);
+                    else probabilities<false>(s[c], sc, ms, cS + 16 * c, sum);
+                };
+                part(0);
+                part(1);
+                part(2);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&b_pa[w]);
+                part(3);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&b_pb[w]);
+                const float2 q = __fadd2_rn(sum[0], sum[1]);
+                l += q.x + q.y;
             }
-            const float ms = m == -INFINITY ? 0.f : m * sc;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float x = fast_exp2(fmaf(s[c][e], sc, -ms)), y = fast_exp2(fmaf(s[c][e + 1], sc, -ms));
-                    sum[(e >> 1) & 3] += x + y;
-                    p[e >> 1] = pack_bf16(x, y);
-                }
-                tmem_st16(cS + 16 * c, p);
+            if (!ok) break;
+            if (n > 0) {
+                if (!(ok = mbar_wait(&b_o[w], no & 1, abort_flag))) break;
+                ++no;
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&b_p[w]);
-        }
-        if (ok && nt[w] > 0) ok = mbar_wait(&b_o[w], 0, abort_flag);
-        if (ok) {
+            __syncwarp();
             tc_fence_after();
-            const int64_t row = (t.q0 + tok) * a.H + hk * a.G + (r - tr * a.G);
-            const int64_t prow = (int64_t)blockIdx.y * a.part_rows + row;
+            const int64_t row = (int64_t)(it.q_tok + x) * a.H + it.hk * a.G + (r - tr * a.G);
+            const int64_t prow = (int64_t)it.z * a.part_rows + row;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN scores stay NaN
             const float lse = l > 0.f ? m * a.scale + log2f(l) * kLn2 : (l == 0.f ? -INFINITY : l);
             if (mine) {
@@ -301,20 +460,19 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             for (int c = 0; c < a.D; c += 32) {
                 float o[32];
-                if (nt[w] > 0) {
+                if (n > 0) {
                     tmem_ld32(cO + c, o);
                     tmem_wait_ld();
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-                if (!mine) continue;
-                if (a.part_o) {
+                if (mine && a.part_o) {
                     float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * a.D + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (c + 4 * e < a.D)
                             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
+                } else if (mine) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * a.D + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -323,13 +481,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                                                 pack_bf16(o[8 * e + 4], o[8 * e + 5]),
                                                 pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                 }
+                __syncwarp();  // the next tensor memory read is the whole warp's
             }
-        } else if (a.status) {
-            atomicExch(a.status, kDevTimeout);
+            tc_fence_before();  // the next item's first product overwrites O after its P arrives
         }
+        if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
     } else {
         setmaxnreg_dec<kOtherRegs>();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
@@ -345,8 +505,9 @@ cudaError_t launch_fwd(const AttnArgs &a, const CUtensorMap &tq, const CUtensorM
     constexpr size_t smem = FwdCfg<DP>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(attn_slots(a.sq, a.N, 1, 2 * R) * a.Hk), a.nsplit);
-    kern<<<grid, kFwdThreads, smem, st>>>(tq, tk, tv, a, R);
+    const int64_t slots = attn_slots(a.sq, a.N, 1, 2 * R), items = slots * a.Hk * a.nsplit;
+    if (items >= ((int64_t)1 << 31) - kSms) return cudaErrorInvalidValue;
+    kern<<<(unsigned)std::min<int64_t>(items, kSms), kFwdThreads, smem, st>>>(tq, tk, tv, a, R, (int)slots);
     return cudaGetLastError();
 }
 
