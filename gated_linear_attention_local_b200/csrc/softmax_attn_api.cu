@@ -70,21 +70,24 @@ cudaError_t launch_fwd(const AttnArgs &a, cudaStream_t st) {
     return a.bf16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, st);
 }
 
-// The one-token step: keys are split so that the GPU is filled, the prefix of all sequences
-// is one sequence of N query tokens, and the parts of a row are joined at the end.
+// The one-token step.  Up to kDecodeMaxGroup query heads a key head the streaming kernel takes
+// the caches (clusters of CTAs, joined inside); above, the forward's tiles take them in parts.
+// The prefix of all sequences is one sequence of N query tokens for the forward, in parts.
 struct DecodePlan {
     sgla_status why = SGLA_ERR_INVALID_ARGUMENT;
+    bool stream = true;
+    int cluster = 1;                  // CTAs a (sequence, key head) of the streaming kernel
     int64_t split = 0, psplit = 0;    // keys per part of a cache, of the prefix
-    int parts = 0, pparts = 0;        // parts of a cache, of the prefix
+    int parts = 0, pparts = 0;        // parts of a cache (0: streaming), of the prefix
     bool direct = false;              // one part: no join
     size_t off_lse = 0, bytes = 0;
 };
 
-int64_t split_keys(int64_t keys, int64_t units) {
-    // enough parts for two CTAs an SM, at least 256 keys each
-    const int64_t want = std::max<int64_t>(1, (2 * 148 + units - 1) / units);
-    const int64_t len = std::max<int64_t>(256, (keys + want - 1) / want);
-    return (len + 63) / 64 * 64;
+// Keys per part so that `units` work items times the parts come near to `target` CTAs, in
+// whole tiles of 128 keys.
+int64_t split_keys(int64_t keys, int64_t units, int64_t target) {
+    const int64_t parts = std::max<int64_t>(1, target / units);
+    return std::max<int64_t>(256, (keys + parts - 1) / parts + 127) / 128 * 128;
 }
 
 DecodePlan decode_plan(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk, int64_t D, sgla_dtype dtype) {
@@ -96,13 +99,31 @@ DecodePlan decode_plan(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk, i
     p.why = SGLA_OK;
     if (N == 0) return p;
     const int64_t G = H / Hk;
-    p.split = split_keys(S, N * Hk);
-    p.parts = (int)std::max<int64_t>(1, (S + p.split - 1) / p.split);
+    // forward work items of one pass over `tokens` query tokens; one persistent CTA an SM for
+    // bf16, two CTAs an SM for fp32
+    auto items = [&](int64_t tokens) {
+        const int64_t R = 2 * (128 / G);
+        return Hk * (dtype == SGLA_BF16 ? (tokens + R - 1) / R : (tokens * G + 63) / 64);
+    };
+    const int64_t target = dtype == SGLA_BF16 ? 148 : 2 * 148;
+    p.stream = G <= kDecodeMaxGroup;
+    if (p.stream) {
+        // Few units: as many CTAs as run at once (two an SM; a second wave would double the
+        // time), at least 128 keys each.  Many: at least four waves, so that unequal lengths
+        // even out, at least 512 keys each (a CTA's fixed cost is some 5 us).
+        const int64_t units = N * Hk;
+        while (p.cluster < 8 && ((units * p.cluster * 2 <= 2 * 148 && S >= 256 * p.cluster) ||
+                                 (units > 148 && units * p.cluster < 8 * 148 && S >= 1024 * p.cluster)))
+            p.cluster *= 2;
+    } else {
+        p.split = split_keys(S, N * items(1), target);
+        p.parts = (int)std::max<int64_t>(1, (S + p.split - 1) / p.split);
+    }
     if (P > 0) {
-        p.psplit = split_keys(P, Hk * ((N * G + 63) / 64));
+        p.psplit = split_keys(P, items(N), target);
         p.pparts = (int)((P + p.psplit - 1) / p.psplit);
     }
-    p.direct = p.parts + p.pparts == 1;
+    p.direct = p.parts + p.pparts <= 1 && P == 0;
     if (!p.direct) {
         const size_t rows = (size_t)(p.parts + p.pparts) * N * H;
         p.off_lse = align_up(rows * D * sizeof(float), 256);
@@ -196,36 +217,39 @@ sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, co
     const sgla_status s = reset_status(device_status, st);
     if (s != SGLA_OK || N == 0) return s;
     AttnArgs a{};
-    a.q = q; a.k = k_cache; a.v = v_cache; a.o = o;
+    a.q = q; a.o = o;
     a.scale = pick_scale(scale, D);
     a.bf16 = dtype == SGLA_BF16;
-    a.N = N;
-    a.sq.T = 1;
-    a.sk.T = S; a.sk.len = lengths;
     a.H = (int)H; a.Hk = (int)Hk; a.G = (int)(H / Hk); a.D = (int)D;
-    a.status = device_status;
-    a.split = p.split; a.nsplit = p.parts;
     a.part_rows = N * H;
     float *part_o = static_cast<float *>(workspace);
     float *part_lse = p.direct ? nullptr : reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_lse);
-    if (!p.direct) {
-        a.part_o = part_o;
-        a.part_lse = part_lse;
-    }
-    ATTN_LAUNCH("softmax_attention_decode", launch_fwd(a, st));
-    if (p.direct) return SGLA_OK;
-    if (P > 0) {  // every query token against the prefix, as one sequence
+    if (P > 0) {  // every query token against the prefix, as one sequence; its parts come first
         a.k = prefix_k; a.v = prefix_v;
         a.N = 1;
         a.sq.T = N;
-        a.sk.T = P; a.sk.len = nullptr;
+        a.sk.T = P;
         a.split = p.psplit; a.nsplit = p.pparts;
-        a.part_o = part_o + (int64_t)p.parts * N * H * D;
-        a.part_lse = part_lse + (int64_t)p.parts * N * H;
+        a.part_o = part_o;
+        a.part_lse = part_lse;
         ATTN_LAUNCH("softmax_attention_prefix", launch_fwd(a, st));
     }
-    ATTN_LAUNCH("softmax_attention_join",
-                launch_attn_join(part_o, part_lse, o, N * H, p.parts + p.pparts, (int)D, a.bf16, st));
+    a.k = k_cache; a.v = v_cache;
+    a.N = N;
+    a.sq.T = 1;
+    a.sk.T = S; a.sk.len = lengths;
+    a.status = device_status;
+    if (p.stream) {
+        ATTN_LAUNCH("softmax_attention_decode", launch_attn_decode(a, p.cluster, p.pparts, st));
+        return SGLA_OK;
+    }
+    a.split = p.split; a.nsplit = p.parts;
+    a.part_o = p.direct ? nullptr : part_o + (int64_t)p.pparts * N * H * D;
+    a.part_lse = p.direct ? nullptr : part_lse + (int64_t)p.pparts * N * H;
+    ATTN_LAUNCH("softmax_attention_decode", launch_fwd(a, st));
+    if (!p.direct)
+        ATTN_LAUNCH("softmax_attention_join",
+                    launch_attn_join(part_o, part_lse, o, N * H, p.parts + p.pparts, (int)D, a.bf16, st));
     return SGLA_OK;
 }
 

@@ -55,10 +55,13 @@ def test_decode_refusals(lib):
     assert dec(q=None) == INV and dec(kc=None) == INV and dec(ln=None) == INV and dec(o=None) == INV
     assert dec(Pn=3) == INV and dec(Pn=3, pk=P) == INV and dec(Pn=-1) == INV and dec(ln=P + 4) == INV
     assert dec(vc=P + 8) == INV and dec(H=3) == INV and dec(D=129) == UNS and dec(D=136) == UNS
-    assert dec(N=1 << 20, S=1 << 11) == UNS and dec(ws=None) == WS and dec(n=100) == WS and dec(ws=P + 16) == INV
+    assert dec(N=1 << 20, S=1 << 11) == UNS
+    for kw in (dict(Pn=500, pk=P, pv=P), dict(H=64, Hk=2)):  # parts to join: a prefix, a large group
+        assert dec(ws=None, **kw) == WS and dec(n=100, **kw) == WS and dec(ws=P + 16, **kw) == INV
     assert dec(N=0) == 0
     size = lib.softmax_attention_decode_workspace_size
-    assert size(2, 5000, 0, 4, 2, 64, L.SGLA_BF16) > 0 and size(2, 5000, 0, 4, 3, 64, L.SGLA_BF16) == 0
+    assert size(2, 5000, 500, 4, 2, 64, L.SGLA_BF16) > 0 and size(2, 5000, 0, 4, 2, 64, L.SGLA_BF16) == 0
+    assert size(2, 5000, 0, 64, 2, 64, L.SGLA_BF16) > 0 and size(2, 5000, 0, 4, 3, 64, L.SGLA_BF16) == 0
 
 
 def test_rotary_refusals(lib):
