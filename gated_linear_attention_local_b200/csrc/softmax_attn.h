@@ -62,8 +62,9 @@ cudaError_t launch_attn_bwd_dq_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_delta(const AttnArgs &a, const void *o, cudaStream_t st);
 
 // One query token a sequence (a.sq.T == 1), G <= kDecodeMaxGroup: clusters of cs CTAs a (sequence,
-// key head); pparts parts of a prefix (a.part_o, a.part_lse, may be 0) join the result.
-constexpr int kDecodeMaxGroup = 16;
+// key head); pparts <= kDecodeMaxParts parts of a prefix (a.part_o, a.part_lse, may
+// be 0) join the result.
+constexpr int kDecodeMaxGroup = 16, kDecodeMaxParts = 148;
 cudaError_t launch_attn_decode(const AttnArgs &a, int cs, int pparts, cudaStream_t st);
 
 // o of `rows` rows from `parts` parts (part_o, part_lse as in AttnArgs)

@@ -86,7 +86,7 @@ struct DecodePlan {
 // Keys per part so that `units` work items times the parts come near to `target` CTAs, in
 // whole tiles of 128 keys.
 int64_t split_keys(int64_t keys, int64_t units, int64_t target) {
-    const int64_t parts = std::max<int64_t>(1, target / units);
+    const int64_t parts = std::min<int64_t>(kDecodeMaxParts, std::max<int64_t>(1, target / units));
     return std::max<int64_t>(256, (keys + parts - 1) / parts + 127) / 128 * 128;
 }
 

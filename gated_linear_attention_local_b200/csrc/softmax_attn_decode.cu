@@ -5,9 +5,9 @@
 // valid keys evenly (the length is read on the device: no split is empty while others wait);
 // each of a CTA's four warps pulls every fourth tile of 16 keys through its own ring of TMA
 // copies and keeps its own maximum, sum and output, with no barrier between warps until the end.
-// Then the warps of a CTA are joined through shared memory, the CTAs of the cluster through
-// distributed shared memory, and the parts of a shared prefix (computed before for the whole
-// batch) are added as further terms, so a step needs one launch besides the prefix's.
+// Then all warps of the cluster are joined through distributed shared memory, with the parts of
+// a shared prefix (computed before for the whole batch) as further terms, so a step needs one
+// launch besides the prefix's.
 //   join: o = sum_p w_p o_p / sum_p w_p l_p, w_p = 2^(m_p - max m), parts in a fixed order.
 //
 // bf16: mma.sync m16n8k16, the G rows padded to 16 (tcgen05 has no tile below 64 rows; the
@@ -49,15 +49,15 @@ struct DecCfg {
     // 24 KB a warp, two CTAs an SM; fp32 with DP = 128 needs 48 KB for three stages
     static constexpr int STAGES = 24576 / STAGE > 3 ? 24576 / STAGE : 3;
     static constexpr uint32_t RING = STAGES * STAGE;        // one warp's ring
-    static constexpr uint32_t OUT = kWarps * RING;          // [16][DP] floats: the CTA's joined output
-    static constexpr uint32_t ML = OUT + 16 * DP * 4;       // [kWarps + 1][16][2]: m, l of the warps, of the CTA
-    static constexpr uint32_t QS = ML + (kWarps + 1) * 16 * 2 * 4;  // fp32: [16][DP] floats q
+    static constexpr uint32_t ML = kWarps * RING;           // [kWarps][16][2]: m, l of the warps
+    static constexpr uint32_t QS = ML + kWarps * 16 * 2 * 4;  // fp32: [16][DP] floats q
     static constexpr uint32_t PS = QS + (sizeof(T) == 4 ? 16 * DP * 4 : 0);   // fp32: [kWarps][16][16] p
     static constexpr uint32_t BARS = PS + (sizeof(T) == 4 ? kWarps * 16 * 16 * 4 : 0);
     static constexpr size_t SMEM = BARS + kWarps * STAGES * 8 + 16 + 1024;
-    static constexpr int MAX_PARTS = 2 * 148;               // of a prefix
-    static_assert(2 * 16 * 4 * (8 + MAX_PARTS) <= kWarps * RING, "the parts' weights fit the rings");
-    static_assert(RING >= 16u * DP * 4, "a warp leaves its output in its ring");
+    // at the end a warp leaves its output, [16][DP] floats, at the head of its ring; behind those
+    // of warps 0 and 1 lie the weights of all parts
+    static constexpr uint32_t TAIL = 16 * DP * 4;
+    static_assert(TAIL + 16 * 4 * (kMaxCluster * kWarps + kDecodeMaxParts) <= RING, "output and weights fit a ring");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -370,46 +370,24 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     __syncwarp();
     float *ml = reinterpret_cast<float *>(sm + C::ML);
     rows.leave(reinterpret_cast<float *>(ring), ml + warp * 32, sc, lane);
-    __syncthreads();
-
-    // the CTA's warps
-    float *out = reinterpret_cast<float *>(sm + C::OUT), *cml = ml + kWarps * 32;
-    for (int i = threadIdx.x; i < a.G * DP; i += 32 * kWarps) {
-        const int g = i / DP;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 32 + 2 * g]);
-        const float base = top == -INFINITY ? 0.f : top;
-        float acc = 0.f, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(ml[w * 32 + 2 * g] - base);
-            l = fmaf(f, ml[w * 32 + 2 * g + 1], l);
-            acc = fmaf(f, reinterpret_cast<const float *>(sm + w * C::RING)[i], acc);
-        }
-        out[i] = acc;
-        if (i == g * DP) {
-            cml[2 * g] = top;
-            cml[2 * g + 1] = l;
-        }
-    }
     if (cs > 1) cluster.sync();
     else __syncthreads();
 
-    // the cluster's CTAs and the prefix's parts; the cluster's threads share the elements
+    // Join: the warps of the cluster's CTAs, then the prefix's parts.  (log2 maximum, later
+    // weight) and l of each part first.
+    const int own = cs * kWarps, parts = own + pparts;
     const int64_t row0 = n * a.H + hk * a.G;
-    // (log2 maximum, weight later) of each part, CTAs of the cluster first; the rings are free
-    float *pm = reinterpret_cast<float *>(sm), *pl = pm + (kMaxCluster + C::MAX_PARTS) * 16;
-    const int parts = cs + pparts;
+    float *pm = reinterpret_cast<float *>(sm + C::TAIL), *pl = reinterpret_cast<float *>(sm + C::RING + C::TAIL);
     for (int i = threadIdx.x; i < parts * a.G; i += 32 * kWarps) {
         const int p = i / a.G, g = i - p * a.G;
         float m, l;
-        if (p < cs) {
-            const float *rml = cluster.map_shared_rank(cml, p);
-            m = rml[2 * g];
-            l = rml[2 * g + 1];
+        if (p < own) {
+            const float2 x = *reinterpret_cast<const float2 *>(
+                cluster.map_shared_rank(ml, p / kWarps) + (p % kWarps) * 32 + 2 * g);
+            m = x.x;
+            l = x.y;
         } else {
-            m = a.part_lse[(p - cs) * a.part_rows + row0 + g] * kLog2e;
+            m = a.part_lse[(p - own) * a.part_rows + row0 + g] * kLog2e;
             l = 1.f;
         }
         pm[p * 16 + g] = m;
@@ -433,26 +411,39 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
         if (lane == 0) pl[g] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN scores: NaN
     }
     __syncthreads();
-    for (int i = rank * 32 * kWarps + threadIdx.x; i < a.G * a.D; i += cs * 32 * kWarps) {
-        const int g = i / a.D, d = i - g * a.D;
-        float acc = 0.f, x[8];
+    // four columns a thread, the cluster's threads share them; eight loads in flight
+    const int quads = a.D / 4;
+    for (int i = rank * 32 * kWarps + threadIdx.x; i < a.G * quads; i += cs * 32 * kWarps) {
+        const int g = i / quads, d = 4 * (i - g * quads);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < parts; p0 += 8) {
+            float4 x[8];
+            float f[8];
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-            x[r] = r < cs ? cluster.map_shared_rank(out, r)[g * DP + d] : 0.f;
+            for (int e = 0; e < 8; ++e) {
+                const int p = p0 + e;
+                f[e] = p < parts ? pm[p * 16 + g] : 0.f;
+                x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f[e] == 0.f) continue;  // (a part of the prefix without a key has no o)
+                const float *src = p < own ? cluster.map_shared_rank(reinterpret_cast<float *>(sm + (p % kWarps) * C::RING),
+                                                                     p / kWarps) + g * DP + d
+                                           : a.part_o + ((p - own) * a.part_rows + row0 + g) * a.D + d;
+                x[e] = *reinterpret_cast<const float4 *>(src);
+            }
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-            if (r < cs) acc = fmaf(pm[r * 16 + g], x[r], acc);
-        for (int p0 = 0; p0 < pparts; p0 += 8) {  // eight loads in flight
-#pragma unroll
-            for (int e = 0; e < 8; ++e)  // a part without a key (weight 0) has no o
-                x[e] = (p0 + e < pparts && pm[(cs + p0 + e) * 16 + g] != 0.f)
-                           ? a.part_o[((p0 + e) * a.part_rows + row0 + g) * a.D + d]
-                           : 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (p0 + e < pparts) acc = fmaf(pm[(cs + p0 + e) * 16 + g], x[e], acc);
+            for (int e = 0; e < 8; ++e) {
+                acc.x = fmaf(f[e], x[e].x, acc.x);
+                acc.y = fmaf(f[e], x[e].y, acc.y);
+                acc.z = fmaf(f[e], x[e].z, acc.z);
+                acc.w = fmaf(f[e], x[e].w, acc.w);
+            }
         }
-        static_cast<T *>(a.o)[(row0 + g) * a.D + d] = from_f32<T>(acc * pl[g]);
+        const float inv = pl[g];
+        T *dst = static_cast<T *>(a.o) + (row0 + g) * a.D + d;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        else
+            *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
     if (cs > 1) cluster.sync();  // this CTA's shared memory has been read
     if (*abort_flag && a.status && threadIdx.x == 0) atomicExch(a.status, kDevTimeout);
