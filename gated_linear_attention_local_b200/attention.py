@@ -24,15 +24,15 @@ __all__ = ["softmax_attention", "softmax_attention_fwd", "softmax_attention_bwd"
 
 def _operands(named):
     """CUDA, contiguous, one of the library's two operand types, one type for all."""
-    dtype = None
-    for name, t in named:
-        _check_cuda(name, t)
-        if dtype is None:
-            dtype = t.dtype
-            if dtype not in _DTYPES:
-                raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
-        elif t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype} like {named[0][0]}, got {t.dtype}")
+    name, t = named[0]
+    _check_cuda(name, t)
+    dtype = t.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    for other, t in named[1:]:
+        _check_cuda(other, t)
+        if t.dtype != dtype:
+            raise TypeError(f"{other} must be {dtype} like {name}, got {t.dtype}")
     return _DTYPES[dtype]
 
 
@@ -77,13 +77,7 @@ def _check_status(device_status):
             raise ValueError("device_status must hold one element")
 
 
-@_on_tensor_device
-def softmax_attention_fwd(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
-    """Softmax attention.  q [B,T,H,D]; k, v [B,S,Hk,D], H a multiple of Hk; or packed [T,H,D] / [1,T,H,D] with
-    cu_seqlens int64 [N+1] on the device (and cu_seqlens_k where the keys are split otherwise).  causal: query i
-    of a sequence sees the keys j <= i + S - T.  device_status: optional int32 CUDA tensor of one element that
-    receives the cu_seqlens check.  Returns (o shaped like q, lse [..., H] fp32); a query that sees no key has
-    o = 0 and lse = -inf."""
+def _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=None):
     N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
     _check_status(device_status)
     o = torch.empty_like(q)
@@ -93,6 +87,16 @@ def softmax_attention_fwd(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_
                                      _stream())
     raise_for_status(st, "softmax_attention_fwd")
     return o, lse
+
+
+@_on_tensor_device
+def softmax_attention_fwd(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
+    """Softmax attention.  q [B,T,H,D]; k, v [B,S,Hk,D], H a multiple of Hk; or packed [T,H,D] / [1,T,H,D] with
+    cu_seqlens int64 [N+1] on the device (and cu_seqlens_k where the keys are split otherwise).  causal: query i
+    of a sequence sees the keys j <= i + S - T.  device_status: optional int32 CUDA tensor of one element that
+    receives the cu_seqlens check.  Returns (o shaped like q, lse [..., H] fp32); a query that sees no key has
+    o = 0 and lse = -inf."""
+    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status)
 
 
 @_on_tensor_device
@@ -124,7 +128,7 @@ class SoftmaxAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
-        o, lse = softmax_attention_fwd(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+        o, lse = _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
         ctx.opts = (causal, scale)
         return o
@@ -144,7 +148,7 @@ def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seql
     gradients are enabled and one of them requires gradients."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
-    return softmax_attention_fwd(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)[0]
+    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)[0]
 
 
 @_on_tensor_device

@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace sgla {
@@ -72,6 +74,20 @@ cudaError_t launch_attn_join(const float *part_o, const float *part_lse, void *o
                              bool bf16, cudaStream_t st);
 
 #ifdef __CUDACC__
+
+// Allow a kernel its dynamic shared memory, once a device (`done`: a bit a device, one word a
+// kernel).  Saves a runtime call on every launch.
+template <typename F>
+cudaError_t allow_smem(F kern, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // The span of sequence n on one side.  Packed batches have one sequence more than the caller
 // gave: index N covers the tokens behind cu[N], which belong to no sequence (their partner

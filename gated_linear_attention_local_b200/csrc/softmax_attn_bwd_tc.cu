@@ -567,7 +567,8 @@ template <int DP>
 cudaError_t launch_dkdv(const AttnArgs &a, const Maps &m, int gb, int R, cudaStream_t st) {
     auto kern = attn_dkdv_tc_kernel<DP>;
     constexpr size_t smem = BwdCfg<DP>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(attn_slots(a.sk, a.N, 1, kTile) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, gb, R);
     return cudaGetLastError();
@@ -577,7 +578,8 @@ template <int DP>
 cudaError_t launch_dq(const AttnArgs &a, const Maps &m, int R, cudaStream_t st) {
     auto kern = attn_dq_tc_kernel<DP>;
     constexpr size_t smem = BwdCfg<DP>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(attn_slots(a.sq, a.N, 1, R) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R);
     return cudaGetLastError();

@@ -454,7 +454,8 @@ cudaError_t launch_rows(const AttnArgs &a, int cs, int pparts, const CUtensorMap
                         cudaStream_t st) {
     auto kern = attn_decode_kernel<T, DP, GM>;
     constexpr size_t smem = DecCfg<T, DP>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * a.Hk * cs));

@@ -503,7 +503,8 @@ cudaError_t launch_fwd(const AttnArgs &a, const CUtensorMap &tq, const CUtensorM
                        cudaStream_t st) {
     auto kern = attn_fwd_tc_kernel<DP>;
     constexpr size_t smem = FwdCfg<DP>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a.sq, a.N, 1, 2 * R), items = slots * a.Hk * a.nsplit;
     if (items >= ((int64_t)1 << 31) - kSms) return cudaErrorInvalidValue;
