@@ -7,30 +7,35 @@
 // atomics, no fp32 copy of dq in memory); the price is that s, do v and p are formed twice,
 // 7 products of the tile instead of 5.
 //
-// dk, dv: one CTA owns 128 keys of one key head and walks the rows that see them in sub-tiles
-// of 64 packed rows (row = token * G + g), two of which are in work at a time:
-//   S^T = K Q^T, dP^T = V dO^T   (128 keys x 64 rows, fp32, tensor memory; a thread a key)
+// dk, dv: one CTA owns 128 keys of one key head and walks the rows that see them in tiles of
+// 128 packed rows (row = token * G + g, R = 128 / G tokens a tile):
+//   S^T = K Q^T, dP^T = V dO^T   (128 keys x 128 rows, fp32, tensor memory; a lane a key)
 //   dV += P^T dO,  dK += dS^T Q  (P^T, dS^T in bf16 over S^T's and dP^T's columns)
-// dq: one CTA owns 128 packed rows and walks the keys they see in sub-tiles of 64:
-//   S = Q K^T, dP = dO V^T, dQ += dS K   (a thread a row)
-// Two warpgroups take the sub-tiles in turn; while one forms p and ds the tensor cores run
-// the other's products.  The tensor pipe executes in issue order, so the products of sub-tile
-// i + 2 may overwrite the scores' columns right after those that read P and dS of sub-tile i.
+// issued as dV(i), S(i+1), dK(i), dP(i+1): p of tile i+1 is formed under dK(i) and dP(i+1), ds
+// under dV(i+1) and S(i+2), with one buffer each (tensor memory is full: 4 x 128 columns).
+// dq: one CTA owns 128 packed rows and walks the keys they see in tiles of 128:
+//   S = Q K^T, dP = dO V^T, dQ += dS K   (a lane a row)
+// issued as S(i+1), dP(i+1), dQ(i); dP has two buffers (dS lies over dP).
+// Two warpgroups share a tile, 64 of its columns each.  The tensor pipe executes in issue
+// order, so a product may overwrite columns that the products issued before it read.
+//
+// Tiles of 128 x 128 because an M = 128 product of 16 columns costs some 64 cycles for any N
+// up to 128: tiles of 64 (tried first) leave half of the tensor rate.
 //
 // P and dS are rounded to bf16 for their products (relative 2^-8 each, averaged over the
-// sum); scores, p, ds, lse, delta and every accumulator are fp32.
+// sum); scores, p, ds, lse, delta and every accumulator are fp32.  A quarter of the
+// exponentials runs on the FMA pipe (see softmax_attn_tc.cuh).
 //
-// Tensor memory (512 columns): S 2 x 64, dP 2 x 64, accumulators from column 256.
-// Shared memory (DP = 128): the CTA's own two tiles 64 KB, a ring of four sub-tile pairs 128 KB.
-// Warps: 0-3 and 4-7 the warpgroups, 8 TMA, 9 MMA.
+// Shared memory (DP = 128): the CTA's own two tiles 64 KB, rings of three X tiles (Q or K, read
+// by the first and the last product of a tile) and two Y tiles (dO or V), 160 KB.
+// Warps: 0-7 the warpgroups, 8 TMA, 9 MMA (10, 11 fill its warpgroup).
 #include <math.h>
 
 #include <algorithm>
 
 #include "softmax_attn.h"
+#include "softmax_attn_tc.cuh"
 #include "tc_path.h"
-#include "tc_ptx.cuh"
-#include "tc_tiles.cuh"
 
 namespace sgla {
 
@@ -38,79 +43,58 @@ using namespace tc;
 
 namespace {
 
-constexpr int kBwdThreads = 320;
-constexpr int kTile = 128, kSub = 64, kStages = 4;
-constexpr uint32_t kSubRegion = kSub * 128;  // [64 rows x 64 bf16], bytes
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBwdThreads = 384;
+constexpr int kTile = 128, kHalf = 64;
+constexpr int kStX = 3, kStY = 2;
 
 template <int DP>
 struct BwdCfg {
     static constexpr int NG = DP / 64;
-    static constexpr uint32_t T = NG * kRegion;      // own tile (128 rows)
-    static constexpr uint32_t ST = NG * kSubRegion;  // sub-tile (64 rows)
+    static constexpr uint32_t T = NG * kRegion;      // a tile of 128 rows
     static constexpr uint32_t A0 = 0, B0 = T;        // own tiles: K, V (dk dv) or Q, dO (dq)
-    static constexpr uint32_t X0 = 2 * T;            // ring: stage s holds X at X0 + 2 s ST, Y one ST further
-    static constexpr uint32_t ROWS = X0 + 2 * kStages * ST;  // [2][128] floats: lse, delta of a sub-tile's rows
+    static constexpr uint32_t X0 = 2 * T, Y0 = X0 + kStX * T;
+    static constexpr uint32_t ROWS = Y0 + kStY * T;  // [128] -lse (log2 units), [128] -delta of a tile's rows
     static constexpr uint32_t BARS = ROWS + 2 * 128 * 4;
     static constexpr uint32_t MISC = BARS + 24 * 8;
     static constexpr size_t SMEM = MISC + 16 + 1024 > 120 * 1024 ? MISC + 16 + 1024 : 120 * 1024;
-    static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_ACC = 256;
+    static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_ACC = 256;  // dk dv: dV, dK; dq: dP's second buffer, dQ
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct BwdBars {
-    uint64_t *own, *full, *empty, *s, *dp, *p, *ds, *done, *drain;
+    uint64_t *own, *full_x, *empty_x, *full_y, *empty_y, *s, *sfree, *dp, *p, *ds, *done, *drain;
     __device__ explicit BwdBars(uint64_t *b)
-        : own(b), full(b + 1), empty(b + 5), s(b + 9), dp(b + 11), p(b + 13), ds(b + 15), done(b + 17), drain(b + 18) {}
+        : own(b), full_x(b + 1), empty_x(b + 4), full_y(b + 7), empty_y(b + 9), s(b + 11), sfree(b + 12), dp(b + 13),
+          p(b + 15), ds(b + 16), done(b + 18), drain(b + 19) {}
     __device__ void init() const {
         mbar_init(own, 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < kStX; ++i) {
+            mbar_init(&full_x[i], 1);
+            mbar_init(&empty_x[i], 1);
         }
+        for (int i = 0; i < kStY; ++i) {
+            mbar_init(&full_y[i], 1);
+            mbar_init(&empty_y[i], 1);
+        }
+        mbar_init(s, 1);
+        mbar_init(sfree, 256);
+        mbar_init(p, 256);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s[i], 1);
             mbar_init(&dp[i], 1);
-            mbar_init(&p[i], 128);
-            mbar_init(&ds[i], 128);
+            mbar_init(&ds[i], 256);
         }
         mbar_init(done, 1);
         mbar_init(drain, 1);
     }
 };
 
-// Zero rows [from, 64) of a sub-tile pair, by one warp.
+// Zero rows [from, 128) of a tile, by one warp.
 template <int NG>
-__device__ __forceinline__ void zero_rows(unsigned char *pair, int from, int lane) {
-    for (int i = lane; i < 2 * NG * kSub * 8; i += 32)
-        if (((i >> 3) & (kSub - 1)) >= from) reinterpret_cast<uint4 *>(pair)[i] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int lane) {
+    for (int i = lane; i < NG * kTile * 8; i += 32)
+        if (((i >> 3) & (kTile - 1)) >= from) reinterpret_cast<uint4 *>(tile)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
-}
-
-__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
-    float x[32], y[32];
-    __syncwarp();
-    tmem_ld32(taddr, x);
-    tmem_ld32(taddr + 32, y);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        v[e] = x[e];
-        v[32 + e] = y[e];
-    }
-}
-
-__device__ __forceinline__ void st64_bf16(uint32_t taddr, const float (&v)[64]) {
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[32 * c + 2 * e], v[32 * c + 2 * e + 1]);
-        tmem_st16(taddr + 16 * c, w);
-    }
-    tmem_wait_st();
 }
 
 // Columns [0, D) of this thread's accumulator row times f, as bf16 to dst (zeros with !any).
@@ -135,33 +119,83 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, _
     }
 }
 
-// Producer: the CTA's own tiles, then the ring.  own(bar) and sub(i, dst, bar) issue the copies.
-template <int DP, typename Own, typename Sub>
+// 32 values as bf16 pairs to 16 columns
+__device__ __forceinline__ void st32_bf16(uint32_t taddr, const float2 (&v)[16]) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[e].x, v[e].y);
+    tmem_st16(taddr, w);
+}
+
+__device__ __forceinline__ void ld_pairs(uint32_t taddr, float2 (&v)[32]) {
+    float x[32], y[32];
+    __syncwarp();
+    tmem_ld32(taddr, x);
+    tmem_ld32(taddr + 32, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        v[e] = make_float2(x[2 * e], x[2 * e + 1]);
+        v[16 + e] = make_float2(y[2 * e], y[2 * e + 1]);
+    }
+}
+
+// The two warps (of the two warpgroups) that share 32 lanes of tensor memory: both have read
+// their halves of the columns before either writes over them.
+__device__ __forceinline__ void pair_sync(int warp) {
+    __syncwarp();
+    tc_fence_before();
+    named_sync(2 + (warp & 3), 64);
+    tc_fence_after();
+}
+
+// Producer: the CTA's own tiles, then X(i), Y(i).  own(bar), x(i, dst, bar), y(...) issue copies.
+template <int DP, typename Own, typename X, typename Y>
 __device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, int n, uint32_t own_bytes,
-                                        uint32_t sub_bytes, volatile int *abort_flag, Own own, Sub sub) {
+                                        uint32_t bytes, volatile int *abort_flag, Own own, X x, Y y) {
     using C = BwdCfg<DP>;
     mbar_arrive_expect_tx(b.own, own_bytes);
     own(b.own);
-    int i = 0;
-    for (; i < n; ++i) {
-        const int st = i % kStages;
-        if (i >= kStages && !mbar_wait_idle(&b.empty[st], ((i / kStages) - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(&b.full[st], sub_bytes);
-        sub(i, sm + C::X0 + 2 * st * C::ST, &b.full[st]);
+    int ix = 0, iy = 0;
+    while (ix < n) {
+        const int sx = ix % kStX, sy = iy % kStY;
+        if (ix >= kStX && !mbar_wait_idle(&b.empty_x[sx], ((ix / kStX) - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(&b.full_x[sx], bytes);
+        x(ix, sm + C::X0 + sx * C::T, &b.full_x[sx]);
+        ++ix;
+        if (iy >= kStY && !mbar_wait_idle(&b.empty_y[sy], ((iy / kStY) - 1) & 1, abort_flag)) break;
+        mbar_arrive_expect_tx(&b.full_y[sy], bytes);
+        y(iy, sm + C::Y0 + sy * C::T, &b.full_y[sy]);
+        ++iy;
     }
     if (*abort_flag) {  // let the copies in flight land before the CTA exits
         mbar_drain(b.own, 0);
-        for (int k = max(0, i - kStages); k < i; ++k) mbar_drain(&b.full[k % kStages], (k / kStages) & 1);
+        for (int k = max(0, ix - kStX); k < ix; ++k) mbar_drain(&b.full_x[k % kStX], (k / kStX) & 1);
+        for (int k = max(0, iy - kStY); k < iy; ++k) mbar_drain(&b.full_y[k % kStY], (k / kStY) & 1);
     }
+}
+
+// D (+)= A B over nk 16-column steps, both K-major in shared memory (scores: 128 x 128)
+template <int DP>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, int nk) {
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk)
+        if (kk < nk)
+            mma_bf16(d, desc_at(ad, (kk >> 2) * kRegion + (kk & 3) * 32), desc_at(bd, (kk >> 2) * kRegion + (kk & 3) * 32),
+                     id, kk > 0 ? 1u : 0u);
+}
+// D (+)= W X, W (bf16, 128 x 128) in tensor memory, X [128 rows][D] in shared memory
+__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t w, uint64_t xd, uint32_t id, bool add) {
+#pragma unroll
+    for (int jj = 0; jj < kTile / 16; ++jj)
+        mma_bf16_tmem_a(d, w + jj * 8, desc_at(xd, jj * 2048), id, (add || jj > 0) ? 1u : 0u);
 }
 
 // ------------------------------------------------------------------------------------ dk, dv
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
-                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a,
-                    int gb, int R) {
-    // a sub-tile: R tokens x gb heads (gb = min(G, 64), R = 64 / gb); G > 64 takes several a token
+                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
     using C = BwdCfg<DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = align1024(smem_raw);
@@ -174,15 +208,11 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     }
     if (!attn_locate(a, false, slot, 1, kTile, t)) return;
     const int64_t j0 = t.row0, off = t.tk - t.tq;
-    const int chunks = (a.G + gb - 1) / gb;
     const int64_t first = a.causal ? max((int64_t)0, j0 - off) : 0;  // first token that sees key j0
-    const int64_t b0 = first / R;                                    // its token block
-    const int n = first < t.tq ? (int)((t.tq + R - 1) / R - b0) * chunks : 0;
-    auto token0 = [&](int i) { return (b0 + i / chunks) * R; };
-    // rows of sub-tile i that exist
-    auto rows_of = [&](int i) {
-        return chunks > 1 ? min(gb, a.G - (i % chunks) * gb) : (int)min64(R, t.tq - token0(i)) * gb;
-    };
+    const int64_t b0 = first / R;                                    // its tile
+    const int n = __reduce_max_sync(0xffffffffu, first < t.tq ? (int)((t.tq + R - 1) / R - b0) : 0);
+    const int tq_left = (int)(t.tq - b0 * R);  // tokens from the first tile on
+    auto rows_of = [&](int i) { return min(R, tq_left - i * R) * a.G; };
 
     const BwdBars b(reinterpret_cast<uint64_t *>(sm + C::BARS));
     float *srow = reinterpret_cast<float *>(sm + C::ROWS);
@@ -194,9 +224,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (R * gb < kSub)  // rows that no copy writes are operands too
-        for (int s = warp; s < kStages; s += kBwdThreads / 32)
-            zero_rows<C::NG>(sm + C::X0 + 2 * s * C::ST, R * gb, lane);
+    if (R * a.G < kTile && warp < kStX + kStY)  // rows that no copy writes are operands too
+        zero_rows<C::NG>(sm + C::X0 + warp * C::T, R * a.G, lane);
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -207,9 +236,10 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 8) {
+        setmaxnreg_dec<kOtherRegs>();
         if (lane == 0 && n > 0)
             produce<DP>(
-                sm, b, n, 2 * C::T, 2u * C::NG * R * gb * 128, abort_flag,
+                sm, b, n, 2 * C::T, (uint32_t)(C::NG * R * a.G * 128), abort_flag,
                 [&](uint64_t *bar) {
                     for (int g = 0; g < C::NG; ++g) {
                         tma_load_3d(sm + C::A0 + g * kRegion, &tk, bar, 64 * g, hk, (int)(t.k0 + j0));
@@ -217,135 +247,162 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     }
                 },
                 [&](int i, unsigned char *dst, uint64_t *bar) {
-                    const int head = hk * a.G + (i % chunks) * gb, tok = (int)(t.q0 + token0(i));
-                    for (int g = 0; g < C::NG; ++g) {
-                        tma_load_3d(dst + g * kSubRegion, &tq, bar, 64 * g, head, tok);
-                        tma_load_3d(dst + C::ST + g * kSubRegion, &tdo, bar, 64 * g, head, tok);
-                    }
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tq, bar, 64 * g, hk * a.G, (int)(t.q0 + (b0 + i) * R));
+                },
+                [&](int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tdo, bar, 64 * g, hk * a.G, (int)(t.q0 + (b0 + i) * R));
                 });
+        __syncwarp();
     } else if (warp == 9) {
+        setmaxnreg_dec<kOtherRegs>();
         if (n > 0) {
-            const uint32_t idS = idesc_bf16_f32(128, kSub, false, false);
+            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
             const int nk = (a.D + 15) / 16;
             const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
             const uint32_t sbase = smem_u32(sm);
+            const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
+            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
             auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-            auto scores = [&](int i) -> bool {
-                const int st = i % kStages, buf = i & 1;
-                if (!wait(&b.full[st], (i / kStages) & 1)) return false;
-                const int rows = rows_of(i);
-                if (rows < R * gb) zero_rows<C::NG>(sm + C::X0 + 2 * st * C::ST, rows, lane);
+            // X(i) or Y(i) landed, with zeros in rows that do not exist
+            auto landed_x = [&](int i) {
+                if (!wait(&b.full_x[i % kStX], (i / kStX) & 1)) return false;
+                if (rows_of(i) < R * a.G) zero_rows<C::NG>(sm + C::X0 + (i % kStX) * C::T, rows_of(i), lane);
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t x = sbase + C::X0 + 2 * st * C::ST;
-                    for (int kk = 0; kk < nk; ++kk)
-                        mma_bf16(tmem + C::COL_S + buf * kSub, kdesc(sbase + C::A0 + (kk >> 2) * kRegion + (kk & 3) * 32),
-                                 kdesc(x + (kk >> 2) * kSubRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                    mma_commit(&b.s[buf]);
-                    for (int kk = 0; kk < nk; ++kk)
-                        mma_bf16(tmem + C::COL_DP + buf * kSub, kdesc(sbase + C::B0 + (kk >> 2) * kRegion + (kk & 3) * 32),
-                                 kdesc(x + C::ST + (kk >> 2) * kSubRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                    mma_commit(&b.dp[buf]);
-                }
-                __syncwarp();
                 return true;
             };
-            auto accumulate = [&](uint32_t acc, uint32_t w, uint32_t x, bool add) {
-#pragma unroll
-                for (int jj = 0; jj < kSub / 16; ++jj)
-                    mma_bf16_tmem_a(tmem + acc, tmem + w + jj * 8, sdesc(x + jj * 2048, kSubRegion, 1024, 2), idA,
-                                    (add || jj > 0) ? 1u : 0u);
+            auto landed_y = [&](int i) {
+                if (!wait(&b.full_y[i % kStY], (i / kStY) & 1)) return false;
+                if (rows_of(i) < R * a.G) zero_rows<C::NG>(sm + C::Y0 + (i % kStY) * C::T, rows_of(i), lane);
+                tc_fence_after();
+                return true;
             };
             bool ok = wait(b.own, 0);
-            for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
-            for (int i = 0; ok && i < n; ++i) {
-                const int st = i % kStages, buf = i & 1;
-                const uint32_t x = sbase + C::X0 + 2 * st * C::ST, ph = (i >> 1) & 1;
-                if (!(ok = wait(&b.p[buf], ph))) break;
-                tc_fence_after();
-                if (lane == 0) accumulate(C::COL_ACC, C::COL_S + buf * kSub, x + C::ST, i > 0);
-                __syncwarp();
-                if (!(ok = wait(&b.ds[buf], ph))) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    accumulate(C::COL_ACC + 128, C::COL_DP + buf * kSub, x, i > 0);
-                    mma_commit(&b.empty[st]);
-                    if (i == n - 1) mma_commit(b.done);
+            for (int i = -1; ok && i < n; ++i) {
+                if (i >= 0) {
+                    if (!(ok = wait(b.p, i & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, (i % kStY) * C::T), idA, i > 0);
+                        mma_commit(&b.empty_y[i % kStY]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (i + 2 < n) ok = scores(i + 2);
+                if (i + 1 < n) {
+                    if (!(ok = landed_x(i + 1))) break;
+                    if (elect_one()) {
+                        issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, ((i + 1) % kStX) * C::T), idS, nk);
+                        mma_commit(b.s);
+                    }
+                    __syncwarp();
+                }
+                if (i >= 0) {
+                    if (!(ok = wait(&b.ds[0], i & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, (i % kStX) * C::T), idA, i > 0);
+                        mma_commit(&b.empty_x[i % kStX]);
+                        if (i == n - 1) mma_commit(b.done);
+                    }
+                    __syncwarp();
+                }
+                if (i + 1 < n) {
+                    if (!(ok = landed_y(i + 1))) break;
+                    if (elect_one()) {
+                        issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, ((i + 1) % kStY) * C::T), idS, nk);
+                        mma_commit(&b.dp[0]);
+                    }
+                    __syncwarp();
+                }
             }
-            if (lane == 0) {
+            __syncwarp();
+            if (elect_one()) {
                 mma_commit(b.drain);
                 mbar_drain(b.drain, 0);
             }
         }
-    } else {
-        const int w = warp >> 2, r = threadIdx.x & 127;
+    } else if (warp < 8) {
+        setmaxnreg_inc<kRowRegs>();
+        const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;  // this warpgroup's columns: rows c0 ..
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t cS = tmem + C::COL_S + w * kSub + lanes, cDP = tmem + C::COL_DP + w * kSub + lanes;
-        float *my = srow + w * 128;  // [64] lse in log2 units, [64] delta
-        const int rr = r & 63, rt = rr / gb, rg = rr - rt * gb;
-        // lse (r < 64) or delta (r >= 64) of row rr of sub-tile i
+        const uint32_t cS = tmem + C::COL_S + lanes, cDP = tmem + C::COL_DP + lanes;
+        const int rt = r / a.G, rg = r - rt * a.G;
+        // -lse (warpgroup 0) or -delta (1) of row r of tile i
+        const int64_t row00 = (t.q0 + b0 * R + rt) * a.H + hk * a.G + rg;
         auto row_value = [&](int i) -> float {
-            if (i >= n || rr >= rows_of(i)) return 0.f;
-            const int64_t row = (t.q0 + token0(i) + rt) * a.H + hk * a.G + (i % chunks) * gb + rg;
-            return r < 64 ? a.lse_in[row] * kLog2e : a.delta[row];
+            if (i >= n || r >= rows_of(i)) return 0.f;
+            const int64_t row = row00 + (int64_t)i * R * a.H;
+            return w == 0 ? -kLog2e * a.lse_in[row] : -a.delta[row];
         };
         const float sc = a.scale * kLog2e;
-        float next = row_value(w);
+        // row c of tile i sees key r iff c >= (j0 + r - off - first token of the tile) * G
+        const int64_t ahead = a.causal ? j0 + r - off - b0 * R : -(int64_t)kTile;
+        float next = row_value(0);
         bool ok = true;
-        for (int i = w; i < n; i += 2) {
-            const uint32_t ph = (i >> 1) & 1;
-            named_sync(1 + w, 128);  // the previous sub-tile's rows have been read
-            my[r] = next;
-            named_sync(1 + w, 128);
-            next = row_value(i + 2);
-            if (!(ok = mbar_wait(&b.s[w], ph, abort_flag))) break;
+        // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
+        for (int i = 0; i < n; ++i) {
+            named_sync(1, 256);  // the previous tile's values have been read
+            srow[threadIdx.x] = next;
+            named_sync(1, 256);
+            next = row_value(i + 1);
+            const int hi = rows_of(i) - c0;
+            const int lo = (int)max((int64_t)0, min64((ahead - (int64_t)i * R) * a.G, kTile)) - c0;
+            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kHalf);
+            ok = ok && mbar_wait(b.s, i & 1, abort_flag);
             tc_fence_after();
-            float p[kSub];
-            ld64(cS, p);
-            // columns (rows) [lo, hi) see key r
-            const int hi = rows_of(i);
-            const int64_t lo64 = a.causal ? (j0 + r - off - token0(i)) * gb : 0;
-            const int lo = chunks > 1 ? (lo64 > 0 ? kSub : 0) : (int)max((int64_t)0, min64(lo64, kSub));
+            float2 p[32];
+            ld_pairs(cS + c0, p);
+            const float2 *l2 = reinterpret_cast<const float2 *>(srow + c0), *d2 = reinterpret_cast<const float2 *>(srow + 128 + c0);
 #pragma unroll
-            for (int c = 0; c < kSub; c += 4) {
-                const float4 l4 = *reinterpret_cast<const float4 *>(my + c);
-                p[c] = fast_exp2(fmaf(p[c], sc, -l4.x));
-                p[c + 1] = fast_exp2(fmaf(p[c + 1], sc, -l4.y));
-                p[c + 2] = fast_exp2(fmaf(p[c + 2], sc, -l4.z));
-                p[c + 3] = fast_exp2(fmaf(p[c + 3], sc, -l4.w));
-            }
-            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kSub);
-            if (masked) {
+            for (int h = 0; h < 2; ++h) {
+                float2 q[16];
 #pragma unroll
-                for (int c = 0; c < kSub; ++c)
-                    if (c < lo || c >= hi) p[c] = 0.f;
+                for (int e = 0; e < 16; ++e) {
+                    const int k = 16 * h + e;
+                    float2 x = __ffma2_rn(p[k], make_float2(sc, sc), l2[k]);
+                    if (masked) {
+                        x.x = (2 * k >= lo && 2 * k < hi) ? fast_exp2(x.x) : 0.f;
+                        x.y = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? fast_exp2(x.y) : 0.f;
+                    } else if ((e & 3) == 3) {
+                        x = exp2_fma(x);
+                    } else {
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                    }
+                    p[k] = q[e] = x;
+                }
+                if (h == 0) pair_sync(warp);  // P lies over S
+                st32_bf16(cS + c0 / 2 + 16 * h, q);
             }
-            st64_bf16(cS, p);
+            tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b.p[w]);
-            if (!(ok = mbar_wait(&b.dp[w], ph, abort_flag))) break;
+            mbar_arrive(b.p);
+            ok = ok && mbar_wait(&b.dp[0], i & 1, abort_flag);
             tc_fence_after();
-            float dp[kSub];
-            ld64(cDP, dp);
+            float2 dp[32];
+            ld_pairs(cDP + c0, dp);
 #pragma unroll
-            for (int c = 0; c < kSub; c += 4) {
-                const float4 d4 = *reinterpret_cast<const float4 *>(my + 64 + c);
-                dp[c] = p[c] * (dp[c] - d4.x);
-                dp[c + 1] = p[c + 1] * (dp[c + 1] - d4.y);
-                dp[c + 2] = p[c + 2] * (dp[c + 2] - d4.z);
-                dp[c + 3] = p[c + 3] * (dp[c + 3] - d4.w);
+            for (int k = 0; k < 32; ++k) {
+                const float2 x = __fadd2_rn(dp[k], d2[k]);
+                dp[k] = make_float2(p[k].x * x.x, p[k].y * x.y);
+                if (masked) {  // (a hidden pair's dp may be anything)
+                    if (!(2 * k >= lo && 2 * k < hi)) dp[k].x = 0.f;
+                    if (!(2 * k + 1 >= lo && 2 * k + 1 < hi)) dp[k].y = 0.f;
+                }
             }
-            if (masked) {
+            pair_sync(warp);  // dS lies over dP
 #pragma unroll
-                for (int c = 0; c < kSub; ++c)
-                    if (c < lo || c >= hi) dp[c] = 0.f;
+            for (int h = 0; h < 2; ++h) {
+                float2 q[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) q[e] = dp[16 * h + e];
+                st32_bf16(cDP + c0 / 2 + 16 * h, q);
             }
-            st64_bf16(cDP, dp);
+            tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b.ds[w]);
+            mbar_arrive(&b.ds[0]);
         }
         if (ok && n > 0) ok = mbar_wait(b.done, 0, abort_flag);
         if (ok) {
@@ -357,6 +414,8 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         } else if (a.status) {
             atomicExch(a.status, kDevTimeout);
         }
+    } else {
+        setmaxnreg_dec<kOtherRegs>();
     }
     __syncwarp();
     tc_fence_before();
@@ -385,7 +444,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     if (!attn_locate(a, true, slot, 1, R, t)) return;
     const int64_t last = min64(t.row0 + R, t.tq) - 1;
     const int64_t seen = a.causal ? min64(t.tk, last + 1 + t.tk - t.tq) : t.tk;
-    const int n = seen > 0 ? (int)((seen + kSub - 1) / kSub) : 0;
+    const int n = __reduce_max_sync(0xffffffffu, seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0);
 
     const BwdBars b(reinterpret_cast<uint64_t *>(sm + C::BARS));
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
@@ -406,9 +465,10 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 8) {
+        setmaxnreg_dec<kOtherRegs>();
         if (lane == 0 && n > 0)
             produce<DP>(
-                sm, b, n, 2u * C::NG * R * a.G * 128, 2 * C::ST, abort_flag,
+                sm, b, n, 2u * C::NG * R * a.G * 128, C::T, abort_flag,
                 [&](uint64_t *bar) {
                     for (int g = 0; g < C::NG; ++g) {
                         tma_load_3d(sm + C::A0 + g * kRegion, &tq, bar, 64 * g, hk * a.G, (int)(t.q0 + t.row0));
@@ -416,66 +476,71 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     }
                 },
                 [&](int i, unsigned char *dst, uint64_t *bar) {
-                    const int tok = (int)(t.k0 + (int64_t)i * kSub);
-                    for (int g = 0; g < C::NG; ++g) {
-                        tma_load_3d(dst + g * kSubRegion, &tk, bar, 64 * g, hk, tok);
-                        tma_load_3d(dst + C::ST + g * kSubRegion, &tv, bar, 64 * g, hk, tok);
-                    }
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tk, bar, 64 * g, hk, (int)(t.k0 + (int64_t)i * kTile));
+                },
+                [&](int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tv, bar, 64 * g, hk, (int)(t.k0 + (int64_t)i * kTile));
                 });
+        __syncwarp();
     } else if (warp == 9) {
+        setmaxnreg_dec<kOtherRegs>();
         if (n > 0) {
-            const uint32_t idS = idesc_bf16_f32(128, kSub, false, false);
+            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
             const int nk = (a.D + 15) / 16;
             const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
             const uint32_t sbase = smem_u32(sm);
+            const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
+            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
             auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-            auto scores = [&](int i) -> bool {
-                const int st = i % kStages, buf = i & 1;
-                if (!wait(&b.full[st], (i / kStages) & 1)) return false;
-                const int64_t left = t.tk - (int64_t)i * kSub;  // keys behind the sequence are operands too
-                if (left < kSub) zero_rows<C::NG>(sm + C::X0 + 2 * st * C::ST, (int)left, lane);
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t x = sbase + C::X0 + 2 * st * C::ST;
-                    for (int kk = 0; kk < nk; ++kk)
-                        mma_bf16(tmem + C::COL_S + buf * kSub, kdesc(sbase + C::A0 + (kk >> 2) * kRegion + (kk & 3) * 32),
-                                 kdesc(x + (kk >> 2) * kSubRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                    mma_commit(&b.s[buf]);
-                    for (int kk = 0; kk < nk; ++kk)
-                        mma_bf16(tmem + C::COL_DP + buf * kSub, kdesc(sbase + C::B0 + (kk >> 2) * kRegion + (kk & 3) * 32),
-                                 kdesc(x + C::ST + (kk >> 2) * kSubRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                    mma_commit(&b.dp[buf]);
-                }
-                __syncwarp();
-                return true;
-            };
             bool ok = wait(b.own, 0);
-            for (int i = 0; ok && i < min(n, 2); ++i) ok = scores(i);
-            for (int i = 0; ok && i < n; ++i) {
-                const int st = i % kStages, buf = i & 1;
-                if (!(ok = wait(&b.ds[buf], (i >> 1) & 1))) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t x = sbase + C::X0 + 2 * st * C::ST;
-#pragma unroll
-                    for (int jj = 0; jj < kSub / 16; ++jj)
-                        mma_bf16_tmem_a(tmem + C::COL_ACC, tmem + C::COL_DP + buf * kSub + jj * 8,
-                                        sdesc(x + jj * 2048, kSubRegion, 1024, 2), idA, (i > 0 || jj > 0) ? 1u : 0u);
-                    mma_commit(&b.empty[st]);
-                    if (i == n - 1) mma_commit(b.done);
+            for (int i = -1; ok && i < n; ++i) {
+                if (i + 1 < n) {
+                    const int x = (i + 1) % kStX, y = (i + 1) % kStY;
+                    if (!(ok = wait(&b.full_x[x], ((i + 1) / kStX) & 1))) break;
+                    const int64_t left = t.tk - (int64_t)(i + 1) * kTile;  // keys behind the sequence are operands too
+                    if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x * C::T, (int)left, lane);
+                    if (i >= 0 && !(ok = wait(b.sfree, i & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x * C::T), idS, nk);
+                        mma_commit(b.s);
+                    }
+                    __syncwarp();
+                    if (!(ok = wait(&b.full_y[y], ((i + 1) / kStY) & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_scores<DP>(tmem + C::COL_DP + ((i + 1) & 1) * 128, dd, desc_at(yk, y * C::T), idS, nk);
+                        mma_commit(&b.dp[(i + 1) & 1]);
+                        mma_commit(&b.empty_y[y]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (i + 2 < n) ok = scores(i + 2);
+                if (i >= 0) {
+                    if (!(ok = wait(&b.ds[i & 1], (i >> 1) & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + (i & 1) * 128,
+                                  desc_at(xm, (i % kStX) * C::T), idA, i > 0);
+                        mma_commit(&b.empty_x[i % kStX]);
+                        if (i == n - 1) mma_commit(b.done);
+                    }
+                    __syncwarp();
+                }
             }
-            if (lane == 0) {
+            __syncwarp();
+            if (elect_one()) {
                 mma_commit(b.drain);
                 mbar_drain(b.drain, 0);
             }
         }
-    } else {
-        const int w = warp >> 2, r = threadIdx.x & 127;
+    } else if (warp < 8) {
+        setmaxnreg_inc<kRowRegs>();
+        const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t cS = tmem + C::COL_S + w * kSub + lanes, cDP = tmem + C::COL_DP + w * kSub + lanes;
+        const uint32_t cS = tmem + C::COL_S + lanes, cDP = tmem + C::COL_DP + lanes;
         const int tr = r / a.G;
         const int64_t tok = t.row0 + tr;
         const bool mine = tr < R && tok < t.tq;
@@ -486,52 +551,80 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         float delta = mine ? a.delta[row] : 0.f;
         const float sc = a.scale * kLog2e;
         bool ok = true;
-        for (int i = w; i < n; i += 2) {
-            const uint32_t ph = (i >> 1) & 1;
-            if (!(ok = mbar_wait(&b.s[w], ph, abort_flag))) break;
+        for (int i = 0; i < n; ++i) {
+            ok = ok && mbar_wait(b.s, i & 1, abort_flag);
             tc_fence_after();
-            float p[kSub];
-            ld64(cS, p);
+            float2 p[32];
+            ld_pairs(cS + c0, p);
+            tc_fence_before();
+            mbar_arrive(b.sfree);
+            const int left = lim - i * kTile - c0;  // of this thread's columns, the first `left` are seen
+            const bool masked = __any_sync(0xffffffffu, left < kHalf);
 #pragma unroll
-            for (int c = 0; c < kSub; ++c) p[c] = fast_exp2(fmaf(p[c], sc, -lse));
-            if (!(ok = mbar_wait(&b.dp[w], ph, abort_flag))) break;
+            for (int k = 0; k < 32; ++k) {
+                float2 x = __ffma2_rn(p[k], make_float2(sc, sc), make_float2(-lse, -lse));
+                if (!masked && (k & 3) == 3) {
+                    x = exp2_fma(x);
+                } else {
+                    x.x = fast_exp2(x.x);
+                    x.y = fast_exp2(x.y);
+                }
+                p[k] = x;
+            }
+            ok = ok && mbar_wait(&b.dp[i & 1], (i >> 1) & 1, abort_flag);
             tc_fence_after();
-            float dp[kSub];
-            ld64(cDP, dp);
-            const int left = lim - i * kSub;
-            if (i == 0 && __any_sync(0xffffffffu, lim > 0 && lim <= kSub)) {
+            float2 dp[32];
+            ld_pairs(cDP + (i & 1) * 128 + c0, dp);
+            if (i == 0 && w == 0 && __any_sync(0xffffffffu, lim > 0 && lim <= kHalf)) {
                 // All keys of such a row are here: delta = sum_j p dp in fp32.  The one from o
                 // carries o's rounding, which for rows with few keys is the largest error of
                 // dq and dk (measured: dq off by 2.5e-3 with it, 2.4e-3 without).
                 float x = 0.f;
 #pragma unroll
-                for (int c = 0; c < kSub; ++c)
-                    if (c < lim) x = fmaf(p[c], dp[c], x);
-                if (lim > 0 && lim <= kSub) {
+                for (int k = 0; k < 32; ++k) {
+                    if (2 * k < lim) x = fmaf(p[k].x, dp[k].x, x);
+                    if (2 * k + 1 < lim) x = fmaf(p[k].y, dp[k].y, x);
+                }
+                if (lim > 0 && lim <= kHalf) {
                     delta = x;
-                    if (mine) a.delta[row] = x;
+                    a.delta[row] = x;
                 }
             }
+            const float2 nd = make_float2(-delta, -delta);
 #pragma unroll
-            for (int c = 0; c < kSub; ++c) dp[c] = p[c] * (dp[c] - delta);
-            if (__any_sync(0xffffffffu, left < kSub)) {
-#pragma unroll
-                for (int c = 0; c < kSub; ++c)
-                    if (c >= left) dp[c] = 0.f;
+            for (int k = 0; k < 32; ++k) {
+                const float2 x = __fadd2_rn(dp[k], nd);
+                dp[k] = make_float2(p[k].x * x.x, p[k].y * x.y);
+                if (masked) {
+                    if (2 * k >= left) dp[k].x = 0.f;
+                    if (2 * k + 1 >= left) dp[k].y = 0.f;
+                }
             }
-            st64_bf16(cDP, dp);
+            pair_sync(warp);  // dS lies over dP
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float2 q[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) q[e] = dp[16 * h + e];
+                st32_bf16(cDP + (i & 1) * 128 + c0 / 2 + 16 * h, q);
+            }
+            tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b.ds[w]);
+            mbar_arrive(&b.ds[i & 1]);
         }
         if (ok && n > 0) ok = mbar_wait(b.done, 0, abort_flag);
         if (ok) {
             tc_fence_after();
-            if (w == 0)
-                store_acc(tmem + C::COL_ACC + lanes, n > 0, mine, static_cast<__nv_bfloat16 *>(a.dq) + row * a.D, a.D,
-                          a.scale);
+            // each warpgroup stores half of the columns
+            const int h0 = w == 0 ? 0 : (a.D + 63) / 64 * 32, h1 = w == 0 ? min(a.D, (a.D + 63) / 64 * 32) : a.D;
+            if (h1 > h0)
+                store_acc(tmem + C::COL_ACC + 128 + h0 + lanes, n > 0, mine,
+                          static_cast<__nv_bfloat16 *>(a.dq) + row * a.D + h0, h1 - h0, a.scale);
         } else if (a.status) {
             atomicExch(a.status, kDevTimeout);
         }
+    } else {
+        setmaxnreg_dec<kOtherRegs>();
     }
     __syncwarp();
     tc_fence_before();
@@ -546,17 +639,17 @@ struct Maps {
     CUtensorMap q, dout, k, v;
 };
 
-// q, dout in boxes of qh heads x qr tokens, k and v in boxes of kr tokens
-cudaError_t make_maps(const AttnArgs &a, int qh, int qr, int kr, Maps &m) {
+// boxes: q, dout G heads x R tokens, k and v 128 tokens
+cudaError_t make_maps(const AttnArgs &a, int R, Maps &m) {
     const int64_t qt = a.sq.cu ? a.sq.T : a.N * a.sq.T, kt = a.sk.cu ? a.sk.T : a.N * a.sk.T;
     cudaError_t e = cudaSuccess;
     if (qt > 0) {
-        if ((e = tc_make_map_rows(&m.q, a.q, qt, a.H, a.D, qh, qr)) != cudaSuccess) return e;
-        if ((e = tc_make_map_rows(&m.dout, a.dout, qt, a.H, a.D, qh, qr)) != cudaSuccess) return e;
+        if ((e = tc_make_map_rows(&m.q, a.q, qt, a.H, a.D, a.G, R)) != cudaSuccess) return e;
+        if ((e = tc_make_map_rows(&m.dout, a.dout, qt, a.H, a.D, a.G, R)) != cudaSuccess) return e;
     }
     if (kt > 0) {
-        if ((e = tc_make_map_rows(&m.k, a.k, kt, a.Hk, a.D, 1, kr)) != cudaSuccess) return e;
-        if ((e = tc_make_map_rows(&m.v, a.v, kt, a.Hk, a.D, 1, kr)) != cudaSuccess) return e;
+        if ((e = tc_make_map_rows(&m.k, a.k, kt, a.Hk, a.D, 1, kTile)) != cudaSuccess) return e;
+        if ((e = tc_make_map_rows(&m.v, a.v, kt, a.Hk, a.D, 1, kTile)) != cudaSuccess) return e;
     }
     if (qt == 0) m.q = m.dout = m.k;  // a side without tokens is never copied
     if (kt == 0) m.k = m.v = m.q;
@@ -564,13 +657,13 @@ cudaError_t make_maps(const AttnArgs &a, int qh, int qr, int kr, Maps &m) {
 }
 
 template <int DP>
-cudaError_t launch_dkdv(const AttnArgs &a, const Maps &m, int gb, int R, cudaStream_t st) {
+cudaError_t launch_dkdv(const AttnArgs &a, const Maps &m, int R, cudaStream_t st) {
     auto kern = attn_dkdv_tc_kernel<DP>;
     constexpr size_t smem = BwdCfg<DP>::SMEM;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(attn_slots(a.sk, a.N, 1, kTile) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, gb, R);
+    kern<<<(unsigned)(attn_slots(a.sk, a.N, 1, kTile) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R);
     return cudaGetLastError();
 }
 
@@ -588,17 +681,17 @@ cudaError_t launch_dq(const AttnArgs &a, const Maps &m, int R, cudaStream_t st) 
 }  // namespace
 
 cudaError_t launch_attn_bwd_dkdv_tc(const AttnArgs &a, cudaStream_t st) {
-    const int gb = std::min(a.G, kSub), R = kSub / gb;
+    const int R = kTile / a.G;
     Maps m;
-    const cudaError_t e = make_maps(a, gb, R, kTile, m);
+    const cudaError_t e = make_maps(a, R, m);
     if (e != cudaSuccess) return e;
-    return a.D <= 64 ? launch_dkdv<64>(a, m, gb, R, st) : launch_dkdv<128>(a, m, gb, R, st);
+    return a.D <= 64 ? launch_dkdv<64>(a, m, R, st) : launch_dkdv<128>(a, m, R, st);
 }
 
 cudaError_t launch_attn_bwd_dq_tc(const AttnArgs &a, cudaStream_t st) {
     const int R = kTile / a.G;
     Maps m;
-    const cudaError_t e = make_maps(a, a.G, R, kSub, m);
+    const cudaError_t e = make_maps(a, R, m);
     if (e != cudaSuccess) return e;
     return a.D <= 64 ? launch_dq<64>(a, m, R, st) : launch_dq<128>(a, m, R, st);
 }

@@ -19,10 +19,9 @@
 // bf16 range (the rounding is relative) carry without loss.
 //
 // Exponentials: 128 x 128 of them take the special-function unit as long as the two products
-// take the tensor cores (1024 cycles), so a quarter goes to the FMA pipe instead: with
-// n = round(x), f = x - n, 2^x = 2^n p3(f), p3 the degree-3 polynomial of least largest relative
-// error on [-1/2, 1/2] (Remez exchange; 7.5e-5, a fiftieth of the rounding of p to bf16 that
-// follows).  A NaN among a row's visible scores makes its maximum and so all its p NaN.
+// take the tensor cores (1024 cycles), so a quarter goes to the FMA pipe instead
+// (softmax_attn_tc.cuh).  A NaN among a row's visible scores makes its maximum and so all its p
+// NaN.
 //
 // p is rounded to bf16 for the product with V (relative 2^-8, averaged over the keys); its sum
 // l, m, S and O are fp32.
@@ -36,9 +35,8 @@
 #include <algorithm>
 
 #include "softmax_attn.h"
+#include "softmax_attn_tc.cuh"
 #include "tc_path.h"
-#include "tc_ptx.cuh"
-#include "tc_tiles.cuh"
 
 namespace sgla {
 
@@ -47,13 +45,9 @@ using namespace tc;
 namespace {
 
 constexpr int kFwdThreads = 384;
-// Registers a thread: 168 at launch; the row warps take 208, the others keep 80
-// (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
-constexpr int kRowRegs = 208, kOtherRegs = 80;
 constexpr int kTile = 128;
 constexpr int kSms = 148;  // one persistent CTA each
 constexpr int kItems = 2;  // item descriptions in flight
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 units the maximum may lag behind
 
@@ -86,21 +80,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// (2^x, 2^y) on the FMA pipe for x, y <= 8, finite: see the head of this file.  Below -126 the
-// result is 2^-126.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-    const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low bits are round(x)
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
-    const float2 t = __fadd2_rn(x, magic);
-    const float2 f = __fadd2_rn(x, __fadd2_rn(magic, make_float2(-t.x, -t.y)));
-    float2 p = __ffma2_rn(f, make_float2(0.0551716685f, 0.0551716685f), make_float2(0.2426111251f, 0.2426111251f));
-    p = __ffma2_rn(p, f, make_float2(0.6932609677f, 0.6932609677f));
-    p = __ffma2_rn(p, f, make_float2(0.9999280572f, 0.9999280572f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
 
 // p of the scores s[0..32) of a row, as bf16 to 16 columns at taddr; their sum onto sum.
