@@ -53,10 +53,11 @@ struct BwdCfg {
     static constexpr uint32_t T = NG * kRegion;      // a tile of 128 rows
     static constexpr uint32_t A0 = 0, B0 = T;        // own tiles: K, V (dk dv) or Q, dO (dq)
     static constexpr uint32_t X0 = 2 * T, Y0 = X0 + kStX * T;
-    static constexpr uint32_t ROWS = Y0 + kStY * T;  // [128] -lse (log2 units), [128] -delta of a tile's rows
-    static constexpr uint32_t BARS = ROWS + 2 * 128 * 4;
+    static constexpr uint32_t ROWS = Y0 + kStY * T;  // [2][128] -lse (log2 units), [128] -delta of a tile's rows
+    static constexpr uint32_t BARS = ROWS + 2 * 256 * 4;
     static constexpr uint32_t MISC = BARS + 24 * 8;
-    static constexpr size_t SMEM = MISC + 16 + 1024 > 120 * 1024 ? MISC + 16 + 1024 : 120 * 1024;
+    // (no slack for alignment: the array is declared with it)
+    static constexpr size_t SMEM = MISC + 16 > 120 * 1024 ? MISC + 16 : 120 * 1024;
     static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_ACC = 256;  // dk dv: dV, dK; dq: dP's second buffer, dQ
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -119,14 +120,6 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, _
     }
 }
 
-// 32 values as bf16 pairs to 16 columns
-__device__ __forceinline__ void st32_bf16(uint32_t taddr, const float2 (&v)[16]) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[e].x, v[e].y);
-    tmem_st16(taddr, w);
-}
-
 __device__ __forceinline__ void ld_pairs(uint32_t taddr, float2 (&v)[32]) {
     float x[32], y[32];
     __syncwarp();
@@ -147,6 +140,52 @@ __device__ __forceinline__ void pair_sync(int warp) {
     tc_fence_before();
     named_sync(2 + (warp & 3), 64);
     tc_fence_after();
+}
+
+// p = 2^(sc s + nl) of 64 scores (in place); with MASKED only columns [lo, hi) are kept, else a
+// quarter of the exponentials goes to the FMA pipe.  nl: one value a column pair.
+template <bool MASKED, typename NL>
+__device__ __forceinline__ void exp_pass(float2 (&p)[32], float sc, NL nl, int lo, int hi) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        float2 x = __ffma2_rn(p[k], make_float2(sc, sc), nl(k));
+        if (!MASKED && (k & 3) == 3) {
+            x = exp2_fma(x);
+        } else {
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+        }
+        if (MASKED) {
+            x.x = (2 * k >= lo && 2 * k < hi) ? x.x : 0.f;
+            x.y = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? x.y : 0.f;
+        }
+        p[k] = x;
+    }
+}
+// ds = p (dp + nd) of 64 columns, into dp; columns outside [lo, hi) are 0 with MASKED (there dp
+// may be anything)
+template <bool MASKED, typename ND>
+__device__ __forceinline__ void ds_pass(const float2 (&p)[32], float2 (&dp)[32], ND nd, int lo, int hi) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        float2 x = __fmul2_rn(p[k], __fadd2_rn(dp[k], nd(k)));
+        if (MASKED) {
+            x.x = (2 * k >= lo && 2 * k < hi) ? x.x : 0.f;
+            x.y = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? x.y : 0.f;
+        }
+        dp[k] = x;
+    }
+}
+// 64 values as bf16 pairs to 32 columns
+__device__ __forceinline__ void st64_bf16(uint32_t taddr, const float2 (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[16 * h + e].x, v[16 * h + e].y);
+        tmem_st16(taddr + 16 * h, w);
+    }
+    tmem_wait_st();
 }
 
 // Producer: the CTA's own tiles, then X(i), Y(i).  own(bar), x(i, dst, bar), y(...) issue copies.
@@ -197,8 +236,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
     using C = BwdCfg<DP>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm = align1024(smem_raw);
+    extern __shared__ __align__(1024) unsigned char smem_bwd[];
+    unsigned char *sm = smem_bwd;
     AttnTile t;
     const int hk = blockIdx.x % a.Hk;
     int64_t slot = blockIdx.x / a.Hk;
@@ -339,68 +378,44 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const float sc = a.scale * kLog2e;
         // row c of tile i sees key r iff c >= (j0 + r - off - first token of the tile) * G
         const int64_t ahead = a.causal ? j0 + r - off - b0 * R : -(int64_t)kTile;
-        float next = row_value(0);
+        srow[threadIdx.x] = row_value(0);
+        float next = row_value(1);
         bool ok = true;
         // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
         for (int i = 0; i < n; ++i) {
-            named_sync(1, 256);  // the previous tile's values have been read
-            srow[threadIdx.x] = next;
+            // tile i's values are written, and those of tile i - 1 have been read
             named_sync(1, 256);
-            next = row_value(i + 1);
+            srow[((i + 1) & 1) * 256 + threadIdx.x] = next;
+            next = row_value(i + 2);
+            const float4 *l4 = reinterpret_cast<const float4 *>(srow + (i & 1) * 256 + c0), *d4 = l4 + 32;
+            auto nl = [&](int k) {
+                const float4 x = l4[k >> 1];
+                return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+            };
+            auto nd = [&](int k) {
+                const float4 x = d4[k >> 1];
+                return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+            };
             const int hi = rows_of(i) - c0;
             const int lo = (int)max((int64_t)0, min64((ahead - (int64_t)i * R) * a.G, kTile)) - c0;
             const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kHalf);
             ok = ok && mbar_wait(b.s, i & 1, abort_flag);
             tc_fence_after();
-            float2 p[32];
+            float2 p[32], dp[32];
             ld_pairs(cS + c0, p);
-            const float2 *l2 = reinterpret_cast<const float2 *>(srow + c0), *d2 = reinterpret_cast<const float2 *>(srow + 128 + c0);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 q[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int k = 16 * h + e;
-                    float2 x = __ffma2_rn(p[k], make_float2(sc, sc), l2[k]);
-                    if (masked) {
-                        x.x = (2 * k >= lo && 2 * k < hi) ? fast_exp2(x.x) : 0.f;
-                        x.y = (2 * k + 1 >= lo && 2 * k + 1 < hi) ? fast_exp2(x.y) : 0.f;
-                    } else if ((e & 3) == 3) {
-                        x = exp2_fma(x);
-                    } else {
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                    }
-                    p[k] = q[e] = x;
-                }
-                if (h == 0) pair_sync(warp);  // P lies over S
-                st32_bf16(cS + c0 / 2 + 16 * h, q);
-            }
-            tmem_wait_st();
+            if (masked) exp_pass<true>(p, sc, nl, lo, hi);
+            else exp_pass<false>(p, sc, nl, lo, hi);
+            pair_sync(warp);  // P lies over S
+            st64_bf16(cS + c0 / 2, p);
             tc_fence_before();
             mbar_arrive(b.p);
             ok = ok && mbar_wait(&b.dp[0], i & 1, abort_flag);
             tc_fence_after();
-            float2 dp[32];
             ld_pairs(cDP + c0, dp);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const float2 x = __fadd2_rn(dp[k], d2[k]);
-                dp[k] = make_float2(p[k].x * x.x, p[k].y * x.y);
-                if (masked) {  // (a hidden pair's dp may be anything)
-                    if (!(2 * k >= lo && 2 * k < hi)) dp[k].x = 0.f;
-                    if (!(2 * k + 1 >= lo && 2 * k + 1 < hi)) dp[k].y = 0.f;
-                }
-            }
+            if (masked) ds_pass<true>(p, dp, nd, lo, hi);
+            else ds_pass<false>(p, dp, nd, lo, hi);
             pair_sync(warp);  // dS lies over dP
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 q[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) q[e] = dp[16 * h + e];
-                st32_bf16(cDP + c0 / 2 + 16 * h, q);
-            }
-            tmem_wait_st();
+            st64_bf16(cDP + c0 / 2, dp);
             tc_fence_before();
             mbar_arrive(&b.ds[0]);
         }
@@ -432,8 +447,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
     using C = BwdCfg<DP>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm = align1024(smem_raw);
+    extern __shared__ __align__(1024) unsigned char smem_bwd[];
+    unsigned char *sm = smem_bwd;
     AttnTile t;
     const int hk = blockIdx.x % a.Hk;
     int64_t slot = gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk;  // the last rows see the most keys
@@ -551,29 +566,21 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         float delta = mine ? a.delta[row] : 0.f;
         const float sc = a.scale * kLog2e;
         bool ok = true;
+        // (as above: no thread leaves the others at a barrier)
         for (int i = 0; i < n; ++i) {
+            const int left = lim - i * kTile - c0;  // of this thread's columns, the first `left` are seen
+            const bool masked = __any_sync(0xffffffffu, left < kHalf);
             ok = ok && mbar_wait(b.s, i & 1, abort_flag);
             tc_fence_after();
-            float2 p[32];
+            float2 p[32], dp[32];
             ld_pairs(cS + c0, p);
             tc_fence_before();
             mbar_arrive(b.sfree);
-            const int left = lim - i * kTile - c0;  // of this thread's columns, the first `left` are seen
-            const bool masked = __any_sync(0xffffffffu, left < kHalf);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                float2 x = __ffma2_rn(p[k], make_float2(sc, sc), make_float2(-lse, -lse));
-                if (!masked && (k & 3) == 3) {
-                    x = exp2_fma(x);
-                } else {
-                    x.x = fast_exp2(x.x);
-                    x.y = fast_exp2(x.y);
-                }
-                p[k] = x;
-            }
+            auto nl = [&](int) { return make_float2(-lse, -lse); };
+            if (masked) exp_pass<true>(p, sc, nl, 0, left);
+            else exp_pass<false>(p, sc, nl, 0, left);
             ok = ok && mbar_wait(&b.dp[i & 1], (i >> 1) & 1, abort_flag);
             tc_fence_after();
-            float2 dp[32];
             ld_pairs(cDP + (i & 1) * 128 + c0, dp);
             if (i == 0 && w == 0 && __any_sync(0xffffffffu, lim > 0 && lim <= kHalf)) {
                 // All keys of such a row are here: delta = sum_j p dp in fp32.  The one from o
@@ -590,25 +597,11 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     a.delta[row] = x;
                 }
             }
-            const float2 nd = make_float2(-delta, -delta);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const float2 x = __fadd2_rn(dp[k], nd);
-                dp[k] = make_float2(p[k].x * x.x, p[k].y * x.y);
-                if (masked) {
-                    if (2 * k >= left) dp[k].x = 0.f;
-                    if (2 * k + 1 >= left) dp[k].y = 0.f;
-                }
-            }
+            auto nd = [&](int) { return make_float2(-delta, -delta); };
+            if (masked) ds_pass<true>(p, dp, nd, 0, left);
+            else ds_pass<false>(p, dp, nd, 0, left);
             pair_sync(warp);  // dS lies over dP
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 q[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) q[e] = dp[16 * h + e];
-                st32_bf16(cDP + (i & 1) * 128 + c0 / 2 + 16 * h, q);
-            }
-            tmem_wait_st();
+            st64_bf16(cDP + (i & 1) * 128 + c0 / 2, dp);
             tc_fence_before();
             mbar_arrive(&b.ds[i & 1]);
         }
