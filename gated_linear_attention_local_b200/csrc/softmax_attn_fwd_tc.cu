@@ -10,9 +10,11 @@
 // once although it overwrites P_w(j).  P_w V_j starts when the first 96 of its 128 keys are
 // written.
 //
-// One CTA per SM takes items in turn (heaviest first); a scheduler warp finds the sequence of
-// the next item and hands out its description while the current one is in work, and the copies
-// and first products of an item run under the epilogue of the one before.
+// The grid has a block for every item, heaviest first, and one CTA fits an SM; a scheduler warp
+// takes over blocks that have not started (clusterlaunchcontrol), finds their sequence and hands
+// out the next item's description while the current one is in work: the copies and first
+// products of an item run under the epilogue of the one before, and unequal items even out
+// (against a fixed share of the items for each CTA: packed prompts 269 -> 206 us).
 //
 // The maximum m of a row is only moved (and O, l rescaled, in tensor memory, by the row's own
 // thread) when it has grown by more than 2^8: until then p <= 2^8, which fp32 sums and the
@@ -46,8 +48,6 @@ namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kTile = 128;
-constexpr int kSms = 148;  // one persistent CTA each
-constexpr int kItems = 2;  // item descriptions in flight
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 units the maximum may lag behind
 
@@ -68,9 +68,9 @@ struct FwdCfg {
     static constexpr int NG = DP / 64;               // 64-column groups of a tile
     static constexpr uint32_t T = NG * kRegion;      // one tile, bytes
     static constexpr uint32_t Q0 = 0, K0 = 2 * T, V0 = 4 * T;
-    static constexpr uint32_t BARS = 6 * T, MISC = BARS + 32 * 8, ITEMS = MISC + 16;
+    static constexpr uint32_t BARS = 6 * T, MISC = BARS + 32 * 8, ITEM = MISC + 32;
     // at least half of an SM's shared memory: the CTA takes all of its tensor memory
-    static constexpr size_t NEED = ITEMS + kItems * sizeof(Item) + 1024;
+    static constexpr size_t NEED = ITEM + sizeof(Item) + 1024;
     static constexpr size_t SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t COL_O = 256;
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -114,9 +114,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint64_t *empty_k = bars + 8, *empty_v = bars + 10;                // [2]
     uint64_t *b_s = bars + 12, *b_o = bars + 14;                       // [2] per row tile: S, O complete
     uint64_t *b_pa = bars + 16, *b_pb = bars + 18;                     // [2] first 96, last 32 keys of P written
-    uint64_t *full_i = bars + 20, *empty_i = bars + 20 + kItems;       // [kItems] descriptions
-    uint64_t *b_drain = bars + 20 + 2 * kItems;
-    Item *items = reinterpret_cast<Item *>(sm + C::ITEMS);
+    uint64_t *full_i = bars + 20, *empty_i = bars + 21;                // the item's description: written, taken
+    uint64_t *b_drain = bars + 22, *b_next = bars + 23;
+    Item *item = reinterpret_cast<Item *>(sm + C::ITEM);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,11 +126,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_init(&b_pa[b], 128);
             mbar_init(&b_pb[b], 128);
         }
-        for (int b = 0; b < kItems; ++b) {
-            mbar_init(&full_i[b], 1);
-            mbar_init(&empty_i[b], 10);  // one arrival a consuming warp
-        }
+        mbar_init(full_i, 1);
+        mbar_init(empty_i, 10);  // one arrival a consuming warp
         mbar_init(b_drain, 1);
+        mbar_init(b_next, 1);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -144,11 +143,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const uint32_t tmem = *tmem_slot;
     // The next item's description, for every lane of a warp; false when there is none.
     auto next_item = [&](int &count, Item &it) -> bool {
-        const int st = count % kItems;
-        if (!mbar_wait(&full_i[st], (count / kItems) & 1, abort_flag)) return false;
-        it = items[st];
+        if (!mbar_wait(full_i, count & 1, abort_flag)) return false;
+        it = *item;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty_i[st]);
+        if (lane == 0) mbar_arrive(empty_i);
         ++count;
         return it.nt[0] >= 0;
     };
@@ -156,20 +154,19 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (warp == 10) {
         // ---------------------------------------------------------------- scheduler
         setmaxnreg_dec<kOtherRegs>();
-        const int per_z = slots * a.Hk, total = per_z * a.nsplit;
+        const int per_z = slots * a.Hk;
         int count = 0;
         bool ok = true;
         auto publish = [&](const Item &it) {
-            const int st = count % kItems;
-            if (count >= kItems) ok = mbar_wait(&empty_i[st], ((count / kItems) - 1) & 1, abort_flag);
-            if (ok && lane == 0) {
-                items[st] = it;
-                mbar_arrive(&full_i[st]);
+            if (lane == 0) {
+                *item = it;
+                mbar_arrive(full_i);
             }
             __syncwarp();
             ++count;
         };
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+        void *answer = sm + C::MISC + 16;
+        for (int u = blockIdx.x, asked = 0; ok && u >= 0;) {
             Item it;
             it.z = u / per_z;
             const int rest = u - it.z * per_z;
@@ -178,21 +175,37 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             int64_t slot = slots - 1 - rest / a.Hk;
             if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
             AttnTile t;
-            if (!attn_locate(a, true, slot, 1, 2 * R, t)) continue;
-            const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
-            it.keys = (int)(ke > kb ? ke - kb : 0);
-            it.q_tok = (int)(t.q0 + t.row0);
-            it.q_left = (int)(t.tq - t.row0);
-            it.k_tok = (int)(t.k0 + kb);
-            it.k_left = (int)(t.tk - kb);
-            it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX / 2), -(int64_t)INT_MAX / 2);
+            const bool work = attn_locate(a, true, slot, 1, 2 * R, t);
+            if (work) {
+                const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
+                it.keys = (int)(ke > kb ? ke - kb : 0);
+                it.q_tok = (int)(t.q0 + t.row0);
+                it.q_left = (int)(t.tq - t.row0);
+                it.k_tok = (int)(t.k0 + kb);
+                it.k_left = (int)(t.tk - kb);
+                it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX / 2), -(int64_t)INT_MAX / 2);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
-                const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
-                it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
+                for (int w = 0; w < 2; ++w) {
+                    const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
+                    const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
+                    it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
+                }
+                publish(it);
+                // ask for the next one when every warp has this one: one item ahead, and no more
+                // than that held back from idle SMs
+                if (!(ok = mbar_wait_idle(empty_i, (count - 1) & 1, abort_flag))) break;
             }
-            publish(it);
+            __syncwarp();
+            if (lane == 0) {
+                fence_proxy_async_smem();  // the last answer has been read
+                mbar_arrive_expect_tx(b_next, 16);
+                next_block_request(answer, b_next);
+            }
+            __syncwarp();
+            if (!(ok = mbar_wait(b_next, asked & 1, abort_flag))) break;
+            ++asked;
+            u = next_block_answer(answer);
+            __syncwarp();
         }
         Item end{};
         end.nt[0] = -1;
@@ -486,8 +499,8 @@ cudaError_t launch_fwd(const AttnArgs &a, const CUtensorMap &tq, const CUtensorM
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a.sq, a.N, 1, 2 * R), items = slots * a.Hk * a.nsplit;
-    if (items >= ((int64_t)1 << 31) - kSms) return cudaErrorInvalidValue;
-    kern<<<(unsigned)std::min<int64_t>(items, kSms), kFwdThreads, smem, st>>>(tq, tk, tv, a, R, (int)slots);
+    if (items >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+    kern<<<(unsigned)items, kFwdThreads, smem, st>>>(tq, tk, tv, a, R, (int)slots);
     return cudaGetLastError();
 }
 

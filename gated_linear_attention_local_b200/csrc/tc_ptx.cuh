@@ -199,6 +199,29 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// Dynamic work distribution (PTX clusterlaunchcontrol): a running block asks for a block of the
+// same grid that has not started yet; if there is one it will never start, and the caller does
+// its work.  The 16-byte answer lands at `resp` (16-byte aligned, shared) and completes 16 bytes
+// on `bar`.  No further request may follow an answer of "none".
+__device__ __forceinline__ void next_block_request(void *resp, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(resp)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The block index x of the answer at `resp`, or -1 for none.
+__device__ __forceinline__ int next_block_answer(const void *resp) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 y, z, w;\n mov.b32 %1, 0;\n ld.shared.b128 h, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(resp))
+        : "memory");
+    return got ? (int)x : -1;
+}
+
 // Named barrier among `count` threads (ids 1..15; 0 is __syncthreads).
 __device__ __forceinline__ void named_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
