@@ -45,24 +45,24 @@ struct AttnArgs {
     float *part_o;        // [part, q tokens * H, D] o of the split's keys alone
     float *part_lse;      // [part, q tokens * H]
     int64_t part_rows;    // q tokens * H
-    // backward
+    // backward (o is only read there)
     const void *dout;
     const float *lse_in;  // [q tokens, H]
     float *delta;         // [q tokens, H] sum_d do o
     void *dq, *dk, *dv;
 };
 
-// CUDA cores
+// CUDA cores, fp32
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_bwd_dkdv_simt(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_bwd_dq_simt(const AttnArgs &a, cudaStream_t st);
-// tensor cores, bf16
+// delta_i = sum_d do_id o_id, one value a row (fp32)
+cudaError_t launch_attn_delta(const AttnArgs &a, cudaStream_t st);
+
+// Tensor cores, bf16.  The dq kernel also forms delta, which the dk dv kernel reads.
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_bwd_dkdv_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_bwd_dq_tc(const AttnArgs &a, cudaStream_t st);
-// delta_i = sum_d do_id o_id, one value a row
-cudaError_t launch_attn_delta(const AttnArgs &a, const void *o, cudaStream_t st);
-
 // One query token a sequence (a.sq.T == 1), G <= kDecodeMaxGroup: clusters of cs CTAs a (sequence,
 // key head); pparts <= kDecodeMaxParts parts of a prefix (a.part_o, a.part_lse, may
 // be 0) join the result.

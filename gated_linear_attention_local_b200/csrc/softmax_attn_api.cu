@@ -182,8 +182,9 @@ sgla_status softmax_attention_bwd(const void *q, const void *k, const void *v, c
     if ((s = reset_status(device_status, st)) != SGLA_OK) return s;
     a.q = q; a.k = k; a.v = v; a.dout = dout; a.lse_in = lse; a.delta = static_cast<float *>(workspace);
     a.dq = dq; a.dk = dk; a.dv = dv;
-    if (q_tokens > 0) ATTN_LAUNCH("softmax_attention_delta", launch_attn_delta(a, o, st));
-    // dq first: it sharpens delta for rows with few keys
+    a.o = const_cast<void *>(o);  // only read
+    if (q_tokens > 0 && !a.bf16) ATTN_LAUNCH("softmax_attention_delta", launch_attn_delta(a, st));
+    // dq first: for bf16 it forms delta as well
     if (q_tokens > 0)
         ATTN_LAUNCH("softmax_attention_dq", a.bf16 ? launch_attn_bwd_dq_tc(a, st) : launch_attn_bwd_dq_simt(a, st));
     if (k_tokens > 0)

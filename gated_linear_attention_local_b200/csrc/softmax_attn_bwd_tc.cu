@@ -26,9 +26,14 @@
 // sum); scores, p, ds, lse, delta and every accumulator are fp32.  A quarter of the
 // exponentials runs on the FMA pipe (see softmax_attn_tc.cuh).
 //
-// Shared memory (DP = 128): the CTA's own two tiles 64 KB, rings of three X tiles (Q or K, read
+// The CTAs stay on their SM and take item after item (Feed, softmax_attn_tc.cuh; against a CTA
+// an item: packed training MEASURED): the copies and first products of an item run under
+// the stores of the one before.
+//
+// Shared memory (DP = 128): the item's own two tiles 64 KB, rings of three X tiles (Q or K, read
 // by the first and the last product of a tile) and two Y tiles (dO or V), 160 KB.
-// Warps: 0-7 the warpgroups, 8 TMA, 9 MMA (10, 11 fill its warpgroup).
+// Warps: 0-7 the warpgroups, 8 TMA, 9 MMA, 10 scheduler (11 fills its warpgroup).
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -55,20 +60,22 @@ struct BwdCfg {
     static constexpr uint32_t X0 = 2 * T, Y0 = X0 + kStX * T;
     static constexpr uint32_t ROWS = Y0 + kStY * T;  // [2][128] -lse (log2 units), [128] -delta of a tile's rows
     static constexpr uint32_t BARS = ROWS + 2 * 256 * 4;
-    static constexpr uint32_t MISC = BARS + 24 * 8;
+    static constexpr uint32_t MISC = BARS + 26 * 8;  // tensor memory address, abort flag, 16 bytes of the feed
+    static constexpr uint32_t ITEM = MISC + 32;
     // (no slack for alignment: the array is declared with it)
-    static constexpr size_t SMEM = MISC + 16 > 120 * 1024 ? MISC + 16 : 120 * 1024;
+    static constexpr size_t SMEM = ITEM + 64 > 120 * 1024 ? ITEM + 64 : 120 * 1024;
     static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_ACC = 256;  // dk dv: dV, dK; dq: dP's second buffer, dQ
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct BwdBars {
-    uint64_t *own, *full_x, *empty_x, *full_y, *empty_y, *s, *sfree, *dp, *p, *ds, *done, *drain;
+    uint64_t *own, *empty_own, *full_x, *empty_x, *full_y, *empty_y, *s, *sfree, *dp, *p, *ds, *done, *drain, *feed;
     __device__ explicit BwdBars(uint64_t *b)
-        : own(b), full_x(b + 1), empty_x(b + 4), full_y(b + 7), empty_y(b + 9), s(b + 11), sfree(b + 12), dp(b + 13),
-          p(b + 15), ds(b + 16), done(b + 18), drain(b + 19) {}
+        : own(b), empty_own(b + 1), full_x(b + 2), empty_x(b + 5), full_y(b + 8), empty_y(b + 10), s(b + 12),
+          sfree(b + 13), dp(b + 14), p(b + 16), ds(b + 17), done(b + 19), drain(b + 20), feed(b + 21) {}
     __device__ void init() const {
         mbar_init(own, 1);
+        mbar_init(empty_own, 1);
         for (int i = 0; i < kStX; ++i) {
             mbar_init(&full_x[i], 1);
             mbar_init(&empty_x[i], 1);
@@ -98,8 +105,9 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int lan
     __syncwarp();
 }
 
-// Columns [0, D) of this thread's accumulator row times f, as bf16 to dst (zeros with !any).
-__device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, __nv_bfloat16 *dst, int D, float f) {
+// Columns [0, D) of this thread's accumulator row times f, as bf16 to dst (zeros with !any; nullptr:
+// not stored).
+__device__ __forceinline__ void store_acc(uint32_t taddr, bool any, __nv_bfloat16 *dst, int D, float f) {
     __syncwarp();
     for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -109,7 +117,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, bool mine, _
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f : 0.f;
-        if (mine)
+        if (dst)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (c + 8 * e < D)
@@ -188,30 +196,48 @@ __device__ __forceinline__ void st64_bf16(uint32_t taddr, const float2 (&v)[32])
     tmem_wait_st();
 }
 
-// Producer: the CTA's own tiles, then X(i), Y(i).  own(bar), x(i, dst, bar), y(...) issue copies.
-template <int DP, typename Own, typename X, typename Y>
-__device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, int n, uint32_t own_bytes,
-                                        uint32_t bytes, volatile int *abort_flag, Own own, X x, Y y) {
+// Producer, one lane: for every item its own tiles, then X(i), Y(i).  own(it, bar), x(it, i, dst,
+// bar), y(...) issue the copies.
+template <int DP, typename Item, typename Own, typename X, typename Y>
+__device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, const Feed<Item> &feed,
+                                        uint32_t own_bytes, uint32_t bytes, int lane, Own own, X x, Y y) {
     using C = BwdCfg<DP>;
-    mbar_arrive_expect_tx(b.own, own_bytes);
-    own(b.own);
-    int ix = 0, iy = 0;
-    while (ix < n) {
-        const int sx = ix % kStX, sy = iy % kStY;
-        if (ix >= kStX && !mbar_wait_idle(&b.empty_x[sx], ((ix / kStX) - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(&b.full_x[sx], bytes);
-        x(ix, sm + C::X0 + sx * C::T, &b.full_x[sx]);
-        ++ix;
-        if (iy >= kStY && !mbar_wait_idle(&b.empty_y[sy], ((iy / kStY) - 1) & 1, abort_flag)) break;
-        mbar_arrive_expect_tx(&b.full_y[sy], bytes);
-        y(iy, sm + C::Y0 + sy * C::T, &b.full_y[sy]);
-        ++iy;
+    volatile int *abort_flag = feed.abort_flag;
+    Item it;
+    int ni = 0, no = 0, nx = 0, ny = 0;  // items, own tiles, X and Y tiles so far
+    Ring<kStX> rx;
+    Ring<kStY> ry;
+    bool ok = true;
+    while (ok && feed.take(ni, it)) {
+        if (lane == 0 && it.n > 0) {
+            if (no > 0) ok = mbar_wait_idle(b.empty_own, (no - 1) & 1, abort_flag);
+            if (ok) {
+                mbar_arrive_expect_tx(b.own, own_bytes);
+                own(it, b.own);
+                ++no;
+            }
+            for (int i = 0; ok && i < it.n; ++i) {
+                if (nx >= kStX && !(ok = mbar_wait_idle(&b.empty_x[rx.s], rx.ph ^ 1u, abort_flag))) break;
+                mbar_arrive_expect_tx(&b.full_x[rx.s], bytes);
+                x(it, i, sm + C::X0 + rx.s * C::T, &b.full_x[rx.s]);
+                rx.step();
+                ++nx;
+                if (ny >= kStY && !(ok = mbar_wait_idle(&b.empty_y[ry.s], ry.ph ^ 1u, abort_flag))) break;
+                mbar_arrive_expect_tx(&b.full_y[ry.s], bytes);
+                y(it, i, sm + C::Y0 + ry.s * C::T, &b.full_y[ry.s]);
+                ry.step();
+                ++ny;
+            }
+        }
+        if (lane == 0) mbar_arrive(feed.want);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    if (*abort_flag) {  // let the copies in flight land before the CTA exits
-        mbar_drain(b.own, 0);
-        for (int k = max(0, ix - kStX); k < ix; ++k) mbar_drain(&b.full_x[k % kStX], (k / kStX) & 1);
-        for (int k = max(0, iy - kStY); k < iy; ++k) mbar_drain(&b.full_y[k % kStY], (k / kStY) & 1);
+    if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA exits
+        if (no > 0) mbar_drain(b.own, (no - 1) & 1);
+        for (int k = max(0, nx - kStX); k < nx; ++k) mbar_drain(&b.full_x[k % kStX], (k / kStX) & 1);
+        for (int k = max(0, ny - kStY); k < ny; ++k) mbar_drain(&b.full_y[k % kStY], (k / kStY) & 1);
     }
+    __syncwarp();
 }
 
 // D (+)= A B over nk 16-column steps, both K-major in shared memory (scores: 128 x 128)
@@ -231,35 +257,40 @@ __device__ __forceinline__ void issue_sum(uint32_t d, uint32_t w, uint64_t xd, u
 }
 
 // ------------------------------------------------------------------------------------ dk, dv
+struct KvItem {
+    int n;       // row tiles that see the item's keys
+    int k_tok;   // first key (128 keys of one key head)
+    int k_left;  // keys of the sequence from there on
+    int q_tok;   // first token of the first row tile
+    int q_left;  // tokens of the sequence from there on
+    int ahead;   // causal: row c of tile i sees key r iff c >= (ahead + r - i R) G
+    int hk;
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
-                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
+                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R,
+                    int slots) {
     using C = BwdCfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_bwd[];
     unsigned char *sm = smem_bwd;
-    AttnTile t;
-    const int hk = blockIdx.x % a.Hk;
-    int64_t slot = blockIdx.x / a.Hk;
-    if (!a.sk.cu) {  // the first keys are seen by the most rows: every sequence's first tiles first
-        const int64_t per = gridDim.x / a.Hk / a.N;
-        slot = (slot % a.N) * per + slot / a.N;
-    }
-    if (!attn_locate(a, false, slot, 1, kTile, t)) return;
-    const int64_t j0 = t.row0, off = t.tk - t.tq;
-    const int64_t first = a.causal ? max((int64_t)0, j0 - off) : 0;  // first token that sees key j0
-    const int64_t b0 = first / R;                                    // its tile
-    const int n = __reduce_max_sync(0xffffffffu, first < t.tq ? (int)((t.tq + R - 1) / R - b0) : 0);
-    const int tq_left = (int)(t.tq - b0 * R);  // tokens from the first tile on
-    auto rows_of = [&](int i) { return min(R, tq_left - i * R) * a.G; };
-
     const BwdBars b(reinterpret_cast<uint64_t *>(sm + C::BARS));
     float *srow = reinterpret_cast<float *>(sm + C::ROWS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
+    const Feed<KvItem> feed{b.feed, b.feed + 1, b.feed + 2, b.feed + 3, sm + C::MISC + 16, reinterpret_cast<KvItem *>(sm + C::ITEM),
+                            abort_flag};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 256) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tdo);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
     if (threadIdx.x == 0) {
         b.init();
+        feed.init();
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -274,161 +305,202 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 8) {
+    if (warp == 10) {
+        // ---------------------------------------------------------------- scheduler
         setmaxnreg_dec<kOtherRegs>();
-        if (lane == 0 && n > 0)
-            produce<DP>(
-                sm, b, n, 2 * C::T, (uint32_t)(C::NG * R * a.G * 128), abort_flag,
-                [&](uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g) {
-                        tma_load_3d(sm + C::A0 + g * kRegion, &tk, bar, 64 * g, hk, (int)(t.k0 + j0));
-                        tma_load_3d(sm + C::B0 + g * kRegion, &tv, bar, 64 * g, hk, (int)(t.k0 + j0));
-                    }
-                },
-                [&](int i, unsigned char *dst, uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(dst + g * kRegion, &tq, bar, 64 * g, hk * a.G, (int)(t.q0 + (b0 + i) * R));
-                },
-                [&](int i, unsigned char *dst, uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(dst + g * kRegion, &tdo, bar, 64 * g, hk * a.G, (int)(t.q0 + (b0 + i) * R));
-                });
-        __syncwarp();
+        feed.run([&](int u, KvItem &it) -> bool {
+            it.hk = u % a.Hk;
+            int64_t slot = u / a.Hk;
+            // the first keys are seen by the most rows: every sequence's first tiles first
+            if (!a.sk.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+            AttnTile t;
+            if (!attn_locate(a, false, slot, 1, kTile, t)) return false;
+            const int64_t off = t.tk - t.tq;
+            const int64_t first = a.causal ? max((int64_t)0, t.row0 - off) : 0;  // first token that sees the first key
+            const int64_t b0 = first / R;                                        // its tile
+            it.n = first < t.tq ? (int)((t.tq + R - 1) / R - b0) : 0;
+            it.k_tok = (int)(t.k0 + t.row0);
+            it.k_left = (int)(t.tk - t.row0);
+            it.q_tok = (int)(t.q0 + b0 * R);
+            it.q_left = (int)(t.tq - b0 * R);
+            it.ahead = a.causal ? (int)max(t.row0 - off - b0 * R, -(int64_t)INT_MAX / 2) : -INT_MAX / 2;
+            return true;
+        });
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- TMA producer
+        setmaxnreg_dec<kOtherRegs>();
+        produce<DP>(
+            sm, b, feed, 2 * C::T, (uint32_t)(C::NG * R * a.G * 128), lane,
+            [&](const KvItem &it, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g) {
+                    tma_load_3d(sm + C::A0 + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok);
+                    tma_load_3d(sm + C::B0 + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok);
+                }
+            },
+            [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g)
+                    tma_load_3d(dst + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
+            },
+            [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g)
+                    tma_load_3d(dst + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
+            });
     } else if (warp == 9) {
+        // ---------------------------------------------------------------- MMA issuer
         setmaxnreg_dec<kOtherRegs>();
-        if (n > 0) {
-            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-            const int nk = (a.D + 15) / 16;
-            const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
-            const uint32_t sbase = smem_u32(sm);
-            const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
-            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
-            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
-            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-            // X(i) or Y(i) landed, with zeros in rows that do not exist
-            auto landed_x = [&](int i) {
-                if (!wait(&b.full_x[i % kStX], (i / kStX) & 1)) return false;
-                if (rows_of(i) < R * a.G) zero_rows<C::NG>(sm + C::X0 + (i % kStX) * C::T, rows_of(i), lane);
-                tc_fence_after();
-                return true;
-            };
-            auto landed_y = [&](int i) {
-                if (!wait(&b.full_y[i % kStY], (i / kStY) & 1)) return false;
-                if (rows_of(i) < R * a.G) zero_rows<C::NG>(sm + C::Y0 + (i % kStY) * C::T, rows_of(i), lane);
-                tc_fence_after();
-                return true;
-            };
-            bool ok = wait(b.own, 0);
+        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+        const int nk = (a.D + 15) / 16;
+        const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
+        const uint32_t sbase = smem_u32(sm);
+        const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
+        const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+        const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
+        auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+        KvItem it;
+        int ni = 0;
+        uint32_t own_ph = 0, ph = 0;  // parity of the item's own tiles; of p and ds of the tile in turn
+        Ring<kStX> x1, x0;            // X of the scores' tile, of the sums' tile
+        Ring<kStY> y1, y0;
+        bool ok = true;
+        while (ok && feed.take(ni, it)) {
+            // the same in every lane; the reduction leaves it in a uniform register
+            const int n = __reduce_max_sync(0xffffffffu, it.n);
+            if (n == 0) continue;
+            // rows of tile i that do not exist are zeroed: 0 * NaN must not arise
+            const int whole = it.q_left / R;  // tiles before the first partial one
+            if (!(ok = wait(b.own, own_ph))) break;
+            own_ph ^= 1u;
             for (int i = -1; ok && i < n; ++i) {
                 if (i >= 0) {
-                    if (!(ok = wait(b.p, i & 1))) break;
+                    if (!(ok = wait(b.p, ph))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, (i % kStY) * C::T), idA, i > 0);
-                        mma_commit(&b.empty_y[i % kStY]);
+                        issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, y0.s * C::T), idA, i > 0);
+                        mma_commit(&b.empty_y[y0.s]);
                     }
                     __syncwarp();
+                    y0.step();
                 }
                 if (i + 1 < n) {
-                    if (!(ok = landed_x(i + 1))) break;
+                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                    tc_fence_after();
                     if (elect_one()) {
-                        issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, ((i + 1) % kStX) * C::T), idS, nk);
+                        issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, x1.s * C::T), idS, nk);
                         mma_commit(b.s);
                     }
                     __syncwarp();
+                    x1.step();
                 }
                 if (i >= 0) {
-                    if (!(ok = wait(&b.ds[0], i & 1))) break;
+                    if (!(ok = wait(&b.ds[0], ph))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, (i % kStX) * C::T), idA, i > 0);
-                        mma_commit(&b.empty_x[i % kStX]);
+                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, x0.s * C::T), idA, i > 0);
+                        mma_commit(&b.empty_x[x0.s]);
                         if (i == n - 1) mma_commit(b.done);
                     }
                     __syncwarp();
+                    x0.step();
+                    ph ^= 1u;
                 }
                 if (i + 1 < n) {
-                    if (!(ok = landed_y(i + 1))) break;
+                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
+                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::Y0 + y1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                    tc_fence_after();
                     if (elect_one()) {
-                        issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, ((i + 1) % kStY) * C::T), idS, nk);
+                        issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, y1.s * C::T), idS, nk);
                         mma_commit(&b.dp[0]);
+                        if (i + 1 == n - 1) mma_commit(b.empty_own);
                     }
                     __syncwarp();
+                    y1.step();
                 }
             }
-            __syncwarp();
-            if (elect_one()) {
-                mma_commit(b.drain);
-                mbar_drain(b.drain, 0);
-            }
+        }
+        __syncwarp();
+        if (elect_one()) {
+            mma_commit(b.drain);
+            mbar_drain(b.drain, 0);
         }
     } else if (warp < 8) {
+        // ---------------------------------------------------------------- p, ds and the stores
         setmaxnreg_inc<kRowRegs>();
         const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;  // this warpgroup's columns: rows c0 ..
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t cS = tmem + C::COL_S + lanes, cDP = tmem + C::COL_DP + lanes;
         const int rt = r / a.G, rg = r - rt * a.G;
-        // -lse (warpgroup 0) or -delta (1) of row r of tile i
-        const int64_t row00 = (t.q0 + b0 * R + rt) * a.H + hk * a.G + rg;
-        auto row_value = [&](int i) -> float {
-            if (i >= n || r >= rows_of(i)) return 0.f;
-            const int64_t row = row00 + (int64_t)i * R * a.H;
-            return w == 0 ? -kLog2e * a.lse_in[row] : -a.delta[row];
-        };
         const float sc = a.scale * kLog2e;
-        // row c of tile i sees key r iff c >= (j0 + r - off - first token of the tile) * G
-        const int64_t ahead = a.causal ? j0 + r - off - b0 * R : -(int64_t)kTile;
-        srow[threadIdx.x] = row_value(0);
-        float next = row_value(1);
+        KvItem it;
+        int ni = 0;
+        uint32_t tile = 0, done_ph = 0;  // tiles so far, parity of done
         bool ok = true;
-        // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
-        for (int i = 0; i < n; ++i) {
-            // tile i's values are written, and those of tile i - 1 have been read
-            named_sync(1, 256);
-            srow[((i + 1) & 1) * 256 + threadIdx.x] = next;
-            next = row_value(i + 2);
-            const float4 *l4 = reinterpret_cast<const float4 *>(srow + (i & 1) * 256 + c0), *d4 = l4 + 32;
-            auto nl = [&](int k) {
-                const float4 x = l4[k >> 1];
-                return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+        // (all row warps go on or none: a warp that gave up must not leave others at a barrier)
+        while (named_all(1, 256, ok && feed.take(ni, it))) {
+            const int n = it.n;
+            auto rows_of = [&](int i) { return min(R, it.q_left - i * R) * a.G; };
+            // -lse (warpgroup 0) or -delta (1) of row r of tile i
+            const int64_t row00 = (int64_t)(it.q_tok + rt) * a.H + it.hk * a.G + rg;
+            auto row_value = [&](int i) -> float {
+                if (i >= n || rt >= R || i * R + rt >= it.q_left) return 0.f;
+                const int64_t row = row00 + (int64_t)i * R * a.H;
+                return w == 0 ? -kLog2e * a.lse_in[row] : -a.delta[row];
             };
-            auto nd = [&](int k) {
-                const float4 x = d4[k >> 1];
-                return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
-            };
-            const int hi = rows_of(i) - c0;
-            const int lo = (int)max((int64_t)0, min64((ahead - (int64_t)i * R) * a.G, kTile)) - c0;
-            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kHalf);
-            ok = ok && mbar_wait(b.s, i & 1, abort_flag);
+            srow[(tile & 1) * 256 + threadIdx.x] = row_value(0);
+            float next = row_value(1);
+            // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
+            for (int i = 0; i < n; ++i, ++tile) {
+                // this tile's values are written, and those of the one before have been read
+                named_sync(1, 256);
+                srow[((tile + 1) & 1) * 256 + threadIdx.x] = next;
+                next = row_value(i + 2);
+                const float4 *l4 = reinterpret_cast<const float4 *>(srow + (tile & 1) * 256 + c0), *d4 = l4 + 32;
+                auto nl = [&](int k) {
+                    const float4 x = l4[k >> 1];
+                    return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+                };
+                auto nd = [&](int k) {
+                    const float4 x = d4[k >> 1];
+                    return k & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+                };
+                const int hi = rows_of(i) - c0;
+                const int64_t lo64 = ((int64_t)it.ahead + r - (int64_t)i * R) * a.G;
+                const int lo = (int)max((int64_t)0, min64(lo64, kTile)) - c0;
+                const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kHalf);
+                ok = ok && mbar_wait(b.s, tile & 1, abort_flag);
+                tc_fence_after();
+                float2 p[32], dp[32];
+                ld_pairs(cS + c0, p);
+                if (masked) exp_pass<true>(p, sc, nl, lo, hi);
+                else exp_pass<false>(p, sc, nl, lo, hi);
+                pair_sync(warp);  // P lies over S
+                st64_bf16(cS + c0 / 2, p);
+                tc_fence_before();
+                mbar_arrive(b.p);
+                ok = ok && mbar_wait(&b.dp[0], tile & 1, abort_flag);
+                tc_fence_after();
+                ld_pairs(cDP + c0, dp);
+                if (masked) ds_pass<true>(p, dp, nd, lo, hi);
+                else ds_pass<false>(p, dp, nd, lo, hi);
+                pair_sync(warp);  // dS lies over dP
+                st64_bf16(cDP + c0 / 2, dp);
+                tc_fence_before();
+                mbar_arrive(&b.ds[0]);
+            }
+            if (n > 0) {
+                ok = ok && mbar_wait(b.done, done_ph, abort_flag);
+                done_ph ^= 1u;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
             tc_fence_after();
-            float2 p[32], dp[32];
-            ld_pairs(cS + c0, p);
-            if (masked) exp_pass<true>(p, sc, nl, lo, hi);
-            else exp_pass<false>(p, sc, nl, lo, hi);
-            pair_sync(warp);  // P lies over S
-            st64_bf16(cS + c0 / 2, p);
-            tc_fence_before();
-            mbar_arrive(b.p);
-            ok = ok && mbar_wait(&b.dp[0], i & 1, abort_flag);
-            tc_fence_after();
-            ld_pairs(cDP + c0, dp);
-            if (masked) ds_pass<true>(p, dp, nd, lo, hi);
-            else ds_pass<false>(p, dp, nd, lo, hi);
-            pair_sync(warp);  // dS lies over dP
-            st64_bf16(cDP + c0 / 2, dp);
-            tc_fence_before();
-            mbar_arrive(&b.ds[0]);
+            __nv_bfloat16 *dst = r < it.k_left ? static_cast<__nv_bfloat16 *>(w == 0 ? a.dv : a.dk) +
+                                                     ((int64_t)(it.k_tok + r) * a.Hk + it.hk) * a.D
+                                               : nullptr;
+            store_acc(tmem + C::COL_ACC + w * 128 + lanes, n > 0, dst, a.D, w == 0 ? 1.f : a.scale);
+            tc_fence_before();  // the next item's first sums overwrite the accumulators after its P arrives
         }
-        if (ok && n > 0) ok = mbar_wait(b.done, 0, abort_flag);
-        if (ok) {
-            tc_fence_after();
-            const bool mine = j0 + r < t.tk;
-            const int64_t o = ((t.k0 + j0 + r) * a.Hk + hk) * a.D;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(w == 0 ? a.dv : a.dk) + (mine ? o : 0);
-            store_acc(tmem + C::COL_ACC + w * 128 + lanes, n > 0, mine, dst, a.D, w == 0 ? 1.f : a.scale);
-        } else if (a.status) {
-            atomicExch(a.status, kDevTimeout);
-        }
+        if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
     } else {
         setmaxnreg_dec<kOtherRegs>();
     }
@@ -442,31 +514,40 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
 }
 
 // ------------------------------------------------------------------------------------ dq
+struct QItem {
+    int n;       // key tiles that the item's rows see
+    int q_tok;   // first token
+    int q_left;  // tokens of the sequence from there on
+    int k_tok;   // first key of the sequence
+    int keys;    // its keys
+    int shift;   // causal: token x of the item sees keys < x + 1 + shift
+    int hk;
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
-                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R) {
+                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R,
+                  int slots) {
     using C = BwdCfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_bwd[];
     unsigned char *sm = smem_bwd;
-    AttnTile t;
-    const int hk = blockIdx.x % a.Hk;
-    int64_t slot = gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk;  // the last rows see the most keys
-    if (!a.sq.cu) {
-        const int64_t per = gridDim.x / a.Hk / a.N;
-        slot = (slot % a.N) * per + slot / a.N;
-    }
-    if (!attn_locate(a, true, slot, 1, R, t)) return;
-    const int64_t last = min64(t.row0 + R, t.tq) - 1;
-    const int64_t seen = a.causal ? min64(t.tk, last + 1 + t.tk - t.tq) : t.tk;
-    const int n = __reduce_max_sync(0xffffffffu, seen > 0 ? (int)((seen + kTile - 1) / kTile) : 0);
-
     const BwdBars b(reinterpret_cast<uint64_t *>(sm + C::BARS));
+    float *srow = reinterpret_cast<float *>(sm + C::ROWS);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
+    const Feed<QItem> feed{b.feed, b.feed + 1, b.feed + 2, b.feed + 3, sm + C::MISC + 16, reinterpret_cast<QItem *>(sm + C::ITEM),
+                           abort_flag};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 256) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tdo);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
+    }
     if (threadIdx.x == 0) {
         b.init();
+        feed.init();
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -479,143 +560,212 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 8) {
+    if (warp == 10) {
+        // ---------------------------------------------------------------- scheduler
         setmaxnreg_dec<kOtherRegs>();
-        if (lane == 0 && n > 0)
-            produce<DP>(
-                sm, b, n, 2u * C::NG * R * a.G * 128, C::T, abort_flag,
-                [&](uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g) {
-                        tma_load_3d(sm + C::A0 + g * kRegion, &tq, bar, 64 * g, hk * a.G, (int)(t.q0 + t.row0));
-                        tma_load_3d(sm + C::B0 + g * kRegion, &tdo, bar, 64 * g, hk * a.G, (int)(t.q0 + t.row0));
-                    }
-                },
-                [&](int i, unsigned char *dst, uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(dst + g * kRegion, &tk, bar, 64 * g, hk, (int)(t.k0 + (int64_t)i * kTile));
-                },
-                [&](int i, unsigned char *dst, uint64_t *bar) {
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(dst + g * kRegion, &tv, bar, 64 * g, hk, (int)(t.k0 + (int64_t)i * kTile));
-                });
-        __syncwarp();
+        feed.run([&](int u, QItem &it) -> bool {
+            it.hk = u % a.Hk;
+            int64_t slot = slots - 1 - u / a.Hk;  // the last rows see the most keys
+            if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+            AttnTile t;
+            if (!attn_locate(a, true, slot, 1, R, t)) return false;
+            it.q_tok = (int)(t.q0 + t.row0);
+            it.q_left = (int)(t.tq - t.row0);
+            it.k_tok = (int)t.k0;
+            it.keys = (int)t.tk;
+            it.shift = (int)max(min64(t.row0 + t.tk - t.tq, INT_MAX - 256), -(int64_t)INT_MAX / 2);
+            const int seen = a.causal ? min(it.keys, min(R, it.q_left) + it.shift) : it.keys;
+            it.n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+            return true;
+        });
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- TMA producer
+        setmaxnreg_dec<kOtherRegs>();
+        produce<DP>(
+            sm, b, feed, 2u * C::NG * R * a.G * 128, C::T, lane,
+            [&](const QItem &it, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g) {
+                    tma_load_3d(sm + C::A0 + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok);
+                    tma_load_3d(sm + C::B0 + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok);
+                }
+            },
+            [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g)
+                    tma_load_3d(dst + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok + i * kTile);
+            },
+            [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                for (int g = 0; g < C::NG; ++g)
+                    tma_load_3d(dst + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok + i * kTile);
+            });
     } else if (warp == 9) {
+        // ---------------------------------------------------------------- MMA issuer
         setmaxnreg_dec<kOtherRegs>();
-        if (n > 0) {
-            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-            const int nk = (a.D + 15) / 16;
-            const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
-            const uint32_t sbase = smem_u32(sm);
-            const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
-            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
-            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
-            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-            bool ok = wait(b.own, 0);
+        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+        const int nk = (a.D + 15) / 16;
+        const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
+        const uint32_t sbase = smem_u32(sm);
+        const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
+        const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+        const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
+        auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+        QItem it;
+        int ni = 0;
+        uint32_t own_ph = 0;
+        Ring<kStX> x1, x0;  // K of the scores' tile, of the sum's tile
+        Ring<kStY> y1;
+        Ring<2> d1, d0;     // dP's buffers, of the scores' tile, of the sum's tile
+        uint32_t free_ph = 1;  // parity of S's release by the tile before the scores' tile
+        bool ok = true;
+        while (ok && feed.take(ni, it)) {
+            const int n = __reduce_max_sync(0xffffffffu, it.n);
+            if (n == 0) continue;
+            if (!(ok = wait(b.own, own_ph))) break;
+            own_ph ^= 1u;
             for (int i = -1; ok && i < n; ++i) {
                 if (i + 1 < n) {
-                    const int x = (i + 1) % kStX, y = (i + 1) % kStY;
-                    if (!(ok = wait(&b.full_x[x], ((i + 1) / kStX) & 1))) break;
-                    const int64_t left = t.tk - (int64_t)(i + 1) * kTile;  // keys behind the sequence are operands too
-                    if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x * C::T, (int)left, lane);
-                    if (i >= 0 && !(ok = wait(b.sfree, i & 1))) break;
+                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                    const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
+                    if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
+                    if (!(ok = wait(b.sfree, free_ph))) break;  // (the very first passes at once)
+                    free_ph ^= 1u;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x * C::T), idS, nk);
+                        issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
                         mma_commit(b.s);
                     }
                     __syncwarp();
-                    if (!(ok = wait(&b.full_y[y], ((i + 1) / kStY) & 1))) break;
+                    x1.step();
+                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_scores<DP>(tmem + C::COL_DP + ((i + 1) & 1) * 128, dd, desc_at(yk, y * C::T), idS, nk);
-                        mma_commit(&b.dp[(i + 1) & 1]);
-                        mma_commit(&b.empty_y[y]);
+                        issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
+                        mma_commit(&b.dp[d1.s]);
+                        mma_commit(&b.empty_y[y1.s]);
+                        if (i + 1 == n - 1) mma_commit(b.empty_own);
                     }
                     __syncwarp();
+                    y1.step();
+                    d1.step();
                 }
                 if (i >= 0) {
-                    if (!(ok = wait(&b.ds[i & 1], (i >> 1) & 1))) break;
+                    if (!(ok = wait(&b.ds[d0.s], d0.ph))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + (i & 1) * 128,
-                                  desc_at(xm, (i % kStX) * C::T), idA, i > 0);
-                        mma_commit(&b.empty_x[i % kStX]);
+                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + d0.s * 128, desc_at(xm, x0.s * C::T), idA,
+                                  i > 0);
+                        mma_commit(&b.empty_x[x0.s]);
                         if (i == n - 1) mma_commit(b.done);
                     }
                     __syncwarp();
+                    x0.step();
+                    d0.step();
                 }
             }
-            __syncwarp();
-            if (elect_one()) {
-                mma_commit(b.drain);
-                mbar_drain(b.drain, 0);
-            }
+        }
+        __syncwarp();
+        if (elect_one()) {
+            mma_commit(b.drain);
+            mbar_drain(b.drain, 0);
         }
     } else if (warp < 8) {
+        // ---------------------------------------------------------------- delta, p, ds and the stores
         setmaxnreg_inc<kRowRegs>();
         const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t cS = tmem + C::COL_S + lanes, cDP = tmem + C::COL_DP + lanes;
-        const int tr = r / a.G;
-        const int64_t tok = t.row0 + tr;
-        const bool mine = tr < R && tok < t.tq;
-        const int64_t lim64 = mine ? (a.causal ? min64(t.tk, tok + 1 + t.tk - t.tq) : t.tk) : 0;
-        const int lim = (int)max((int64_t)0, lim64);
-        const int64_t row = mine ? (t.q0 + tok) * a.H + hk * a.G + (r - tr * a.G) : 0;
-        const float lse = mine ? a.lse_in[row] * kLog2e : 0.f;
-        float delta = mine ? a.delta[row] : 0.f;
+        const int tr = r / a.G, tg = r - tr * a.G;
         const float sc = a.scale * kLog2e;
+        // the 16-byte pieces of a row that this warpgroup takes for delta
+        const int pieces = a.D / 8, piece0 = w == 0 ? 0 : (pieces + 1) / 2, piece1 = w == 0 ? (pieces + 1) / 2 : pieces;
+        QItem it;
+        int ni = 0;
+        uint32_t tile = 0, done_ph = 0;
         bool ok = true;
-        // (as above: no thread leaves the others at a barrier)
-        for (int i = 0; i < n; ++i) {
-            const int left = lim - i * kTile - c0;  // of this thread's columns, the first `left` are seen
-            const bool masked = __any_sync(0xffffffffu, left < kHalf);
-            ok = ok && mbar_wait(b.s, i & 1, abort_flag);
-            tc_fence_after();
-            float2 p[32], dp[32];
-            ld_pairs(cS + c0, p);
-            tc_fence_before();
-            mbar_arrive(b.sfree);
-            auto nl = [&](int) { return make_float2(-lse, -lse); };
-            if (masked) exp_pass<true>(p, sc, nl, 0, left);
-            else exp_pass<false>(p, sc, nl, 0, left);
-            ok = ok && mbar_wait(&b.dp[i & 1], (i >> 1) & 1, abort_flag);
-            tc_fence_after();
-            ld_pairs(cDP + (i & 1) * 128 + c0, dp);
-            if (i == 0 && w == 0 && __any_sync(0xffffffffu, lim > 0 && lim <= kHalf)) {
-                // All keys of such a row are here: delta = sum_j p dp in fp32.  The one from o
-                // carries o's rounding, which for rows with few keys is the largest error of
-                // dq and dk (measured: dq off by 2.5e-3 with it, 2.4e-3 without).
-                float x = 0.f;
+        // (all row warps go on or none: a warp that gave up must not leave others at a barrier)
+        while (named_all(1, 256, ok && feed.take(ni, it))) {
+            const int n = it.n;
+            const bool mine = tr < R && tr < it.q_left;
+            const int lim = mine ? max(0, a.causal ? min(it.keys, tr + 1 + it.shift) : it.keys) : 0;
+            const int64_t row = mine ? (int64_t)(it.q_tok + tr) * a.H + it.hk * a.G + tg : 0;
+            const float lse = mine ? a.lse_in[row] * kLog2e : 0.f;
+            // delta = sum_d do o, half of the row in each warpgroup
+            float delta = 0.f;
+            if (mine) {
+                const uint4 *g4 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + row * a.D);
+                const uint4 *o4 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + row * a.D);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (2 * k < lim) x = fmaf(p[k].x, dp[k].x, x);
-                    if (2 * k + 1 < lim) x = fmaf(p[k].y, dp[k].y, x);
-                }
-                if (lim > 0 && lim <= kHalf) {
-                    delta = x;
-                    a.delta[row] = x;
+                for (int e = 0; e < 8; ++e) {
+                    if (piece0 + e >= piece1) continue;
+                    const uint4 g = g4[piece0 + e], o = o4[piece0 + e];
+                    const uint32_t gs[4] = {g.x, g.y, g.z, g.w}, os[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gs[k]));
+                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&os[k]));
+                        delta = fmaf(x.x, y.x, delta);
+                        delta = fmaf(x.y, y.y, delta);
+                    }
                 }
             }
-            auto nd = [&](int) { return make_float2(-delta, -delta); };
-            if (masked) ds_pass<true>(p, dp, nd, 0, left);
-            else ds_pass<false>(p, dp, nd, 0, left);
-            pair_sync(warp);  // dS lies over dP
-            st64_bf16(cDP + (i & 1) * 128 + c0 / 2, dp);
-            tc_fence_before();
-            mbar_arrive(&b.ds[i & 1]);
-        }
-        if (ok && n > 0) ok = mbar_wait(b.done, 0, abort_flag);
-        if (ok) {
+            __syncwarp();
+            srow[(ni & 1) * 256 + threadIdx.x] = delta;  // (the other half belongs to the item before)
+            pair_sync(warp);
+            delta += srow[(ni & 1) * 256 + (threadIdx.x ^ 128)];
+            if (mine && w == 0) a.delta[row] = delta;
+            // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
+            for (int i = 0; i < n; ++i, ++tile) {
+                const int left = lim - i * kTile - c0;  // of this thread's columns, the first `left` are seen
+                const bool masked = __any_sync(0xffffffffu, left < kHalf);
+                ok = ok && mbar_wait(b.s, tile & 1, abort_flag);
+                tc_fence_after();
+                float2 p[32], dp[32];
+                ld_pairs(cS + c0, p);
+                tc_fence_before();
+                mbar_arrive(b.sfree);
+                auto nl = [&](int) { return make_float2(-lse, -lse); };
+                if (masked) exp_pass<true>(p, sc, nl, 0, left);
+                else exp_pass<false>(p, sc, nl, 0, left);
+                ok = ok && mbar_wait(&b.dp[tile & 1], (tile >> 1) & 1, abort_flag);
+                tc_fence_after();
+                ld_pairs(cDP + (tile & 1) * 128 + c0, dp);
+                if (i == 0 && w == 0 && __any_sync(0xffffffffu, lim > 0 && lim <= kHalf)) {
+                    // All keys of such a row are here: delta = sum_j p dp in fp32.  The one from o
+                    // carries o's rounding, which for rows with few keys is the largest error of
+                    // dq and dk (measured: dq off by 2.5e-3 with it, 2.4e-3 without).
+                    float x = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (2 * k < lim) x = fmaf(p[k].x, dp[k].x, x);
+                        if (2 * k + 1 < lim) x = fmaf(p[k].y, dp[k].y, x);
+                    }
+                    if (lim > 0 && lim <= kHalf) {
+                        delta = x;
+                        a.delta[row] = x;
+                    }
+                    __syncwarp();
+                }
+                auto nd = [&](int) { return make_float2(-delta, -delta); };
+                if (masked) ds_pass<true>(p, dp, nd, 0, left);
+                else ds_pass<false>(p, dp, nd, 0, left);
+                pair_sync(warp);  // dS lies over dP
+                st64_bf16(cDP + (tile & 1) * 128 + c0 / 2, dp);
+                tc_fence_before();
+                mbar_arrive(&b.ds[tile & 1]);
+            }
+            if (n > 0) {
+                ok = ok && mbar_wait(b.done, done_ph, abort_flag);
+                done_ph ^= 1u;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
             tc_fence_after();
             // each warpgroup stores half of the columns
-            const int h0 = w == 0 ? 0 : (a.D + 63) / 64 * 32, h1 = w == 0 ? min(a.D, (a.D + 63) / 64 * 32) : a.D;
-            if (h1 > h0)
-                store_acc(tmem + C::COL_ACC + 128 + h0 + lanes, n > 0, mine,
-                          static_cast<__nv_bfloat16 *>(a.dq) + row * a.D + h0, h1 - h0, a.scale);
-        } else if (a.status) {
-            atomicExch(a.status, kDevTimeout);
+            const int h0 = w == 0 ? 0 : 64, h1 = w == 0 ? min(a.D, 64) : a.D;
+            __nv_bfloat16 *dst = mine ? static_cast<__nv_bfloat16 *>(a.dq) + row * a.D + h0 : nullptr;
+            if (h1 > h0) store_acc(tmem + C::COL_ACC + 128 + h0 + lanes, n > 0, dst, h1 - h0, a.scale);
+            tc_fence_before();  // the next item's first sum overwrites the accumulator after its dS arrives
         }
+        if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
     } else {
         setmaxnreg_dec<kOtherRegs>();
     }
@@ -656,7 +806,9 @@ cudaError_t launch_dkdv(const AttnArgs &a, const Maps &m, int R, cudaStream_t st
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(attn_slots(a.sk, a.N, 1, kTile) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R);
+    const int64_t slots = attn_slots(a.sk, a.N, 1, kTile);
+    if (slots * a.Hk >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots);
     return cudaGetLastError();
 }
 
@@ -667,7 +819,9 @@ cudaError_t launch_dq(const AttnArgs &a, const Maps &m, int R, cudaStream_t st) 
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(attn_slots(a.sq, a.N, 1, R) * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R);
+    const int64_t slots = attn_slots(a.sq, a.N, 1, R);
+    if (slots * a.Hk >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots);
     return cudaGetLastError();
 }
 

@@ -53,7 +53,8 @@ constexpr float kGrow = 8.f;  // log2 units the maximum may lag behind
 
 // What the roles need to know of a work item; every count fits 32 bits.
 struct Item {
-    int nt[2];     // key tiles of each row tile; nt[0] < 0: no more items
+    int n;         // key tiles of the item (the larger of nt); < 0: no more items
+    int nt[2];     // key tiles of each row tile
     int q_tok;     // first token of row tile 0
     int q_left;    // tokens of the sequence from there on
     int k_tok;     // first key of this split
@@ -114,11 +115,11 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint64_t *empty_k = bars + 8, *empty_v = bars + 10;                // [2]
     uint64_t *b_s = bars + 12, *b_o = bars + 14;                       // [2] per row tile: S, O complete
     uint64_t *b_pa = bars + 16, *b_pb = bars + 18;                     // [2] first 96, last 32 keys of P written
-    uint64_t *full_i = bars + 20, *empty_i = bars + 21;                // the item's description: written, taken
-    uint64_t *b_drain = bars + 22, *b_next = bars + 23;
-    Item *item = reinterpret_cast<Item *>(sm + C::ITEM);
+    uint64_t *b_drain = bars + 23;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
+    const Feed<Item> feed{bars + 20, bars + 21, bars + 22, bars + 24, sm + C::MISC + 16, reinterpret_cast<Item *>(sm + C::ITEM),
+                          abort_flag};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int b = 0; b < 16; ++b) mbar_init(&bars[b], 1);
@@ -126,12 +127,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_init(&b_pa[b], 128);
             mbar_init(&b_pb[b], 128);
         }
-        mbar_init(full_i, 1);
-        mbar_init(empty_i, 10);  // one arrival a consuming warp
+        feed.init();
         mbar_init(b_drain, 1);
-        mbar_init(b_next, 1);
         *abort_flag = 0;
         mbar_fence_init();
+    }
+    if (threadIdx.x == 256) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+        prefetch_tmap(&tv);
     }
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
@@ -141,33 +145,11 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // The next item's description, for every lane of a warp; false when there is none.
-    auto next_item = [&](int &count, Item &it) -> bool {
-        if (!mbar_wait(full_i, count & 1, abort_flag)) return false;
-        it = *item;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty_i);
-        ++count;
-        return it.nt[0] >= 0;
-    };
-
     if (warp == 10) {
         // ---------------------------------------------------------------- scheduler
         setmaxnreg_dec<kOtherRegs>();
         const int per_z = slots * a.Hk;
-        int count = 0;
-        bool ok = true;
-        auto publish = [&](const Item &it) {
-            if (lane == 0) {
-                *item = it;
-                mbar_arrive(full_i);
-            }
-            __syncwarp();
-            ++count;
-        };
-        void *answer = sm + C::MISC + 16;
-        for (int u = blockIdx.x, asked = 0; ok && u >= 0;) {
-            Item it;
+        feed.run([&](int u, Item &it) -> bool {
             it.z = u / per_z;
             const int rest = u - it.z * per_z;
             it.hk = rest % a.Hk;
@@ -175,41 +157,23 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             int64_t slot = slots - 1 - rest / a.Hk;
             if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
             AttnTile t;
-            const bool work = attn_locate(a, true, slot, 1, 2 * R, t);
-            if (work) {
-                const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
-                it.keys = (int)(ke > kb ? ke - kb : 0);
-                it.q_tok = (int)(t.q0 + t.row0);
-                it.q_left = (int)(t.tq - t.row0);
-                it.k_tok = (int)(t.k0 + kb);
-                it.k_left = (int)(t.tk - kb);
-                it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX / 2), -(int64_t)INT_MAX / 2);
+            if (!attn_locate(a, true, slot, 1, 2 * R, t)) return false;
+            const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
+            it.keys = (int)(ke > kb ? ke - kb : 0);
+            it.q_tok = (int)(t.q0 + t.row0);
+            it.q_left = (int)(t.tq - t.row0);
+            it.k_tok = (int)(t.k0 + kb);
+            it.k_left = (int)(t.tk - kb);
+            it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX / 2), -(int64_t)INT_MAX / 2);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
-                    const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
-                    it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
-                }
-                publish(it);
-                // ask for the next one when every warp has this one: one item ahead, and no more
-                // than that held back from idle SMs
-                if (!(ok = mbar_wait_idle(empty_i, (count - 1) & 1, abort_flag))) break;
+            for (int w = 0; w < 2; ++w) {
+                const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
+                const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
+                it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
             }
-            __syncwarp();
-            if (lane == 0) {
-                fence_proxy_async_smem();  // the last answer has been read
-                mbar_arrive_expect_tx(b_next, 16);
-                next_block_request(answer, b_next);
-            }
-            __syncwarp();
-            if (!(ok = mbar_wait(b_next, asked & 1, abort_flag))) break;
-            ++asked;
-            u = next_block_answer(answer);
-            __syncwarp();
-        }
-        Item end{};
-        end.nt[0] = -1;
-        if (ok) publish(end);
+            it.n = max(it.nt[0], it.nt[1]);
+            return true;
+        });
     } else if (warp == 8) {
         // ---------------------------------------------------------------- TMA producer
         setmaxnreg_dec<kOtherRegs>();
@@ -217,19 +181,20 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         Item it;
         int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
         bool ok = true;
-        while (ok && next_item(ni, it)) {
+        while (ok && feed.take(ni, it)) {
             if (lane == 0) {
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (it.nt[w] == 0) continue;
-                    if (nq[w] > 0 && !(ok = mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag))) break;
+                auto load_q = [&](int w) {
+                    if (it.nt[w] == 0) return true;
+                    if (nq[w] > 0 && !mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag)) return false;
                     mbar_arrive_expect_tx(&full_q[w], qbytes);
                     for (int g = 0; g < C::NG; ++g)
                         tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, it.hk * a.G,
                                     it.q_tok + w * R);
                     ++nq[w];
-                }
-                const int n = max(it.nt[0], it.nt[1]);
-                for (int j = 0; ok && j < n; ++j) {
+                    return true;
+                };
+                ok = load_q(0);
+                for (int j = 0; ok && j < it.n; ++j) {
                     const int st = kv & 1;
                     const uint32_t ph = ((kv >> 1) - 1) & 1;
                     if (kv >= 2 && !(ok = mbar_wait_idle(&empty_k[st], ph, abort_flag))) break;
@@ -238,6 +203,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, it.hk,
                                     it.k_tok + j * kTile);
                     ++kv;
+                    if (j == 0 && !(ok = load_q(1))) break;
                     if (nv >= 2 && !(ok = mbar_wait_idle(&empty_v[st], ph, abort_flag))) break;
                     mbar_arrive_expect_tx(&full_v[st], C::T);
                     for (int g = 0; g < C::NG; ++g)
@@ -246,6 +212,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     ++nv;
                 }
             }
+            if (lane == 0) mbar_arrive(feed.want);
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA exits
@@ -267,7 +234,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         Item it;
         int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
         bool ok = true;
-        while (ok && next_item(ni, it)) {
+        while (ok && feed.take(ni, it)) {
             // the same in every lane; the reduction leaves them in uniform registers, from which
             // the products' descriptors are formed without a move per operand
             const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
@@ -363,7 +330,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         Item it;
         int ni = 0, ns = 0, no = 0;
         bool ok = true;
-        while (ok && next_item(ni, it)) {
+        while (ok && feed.take(ni, it)) {
             const bool mine = tr < R && x < it.q_left;
             const int n = it.nt[w];
             const int lim = mine ? (a.causal ? min(it.keys, x + 1 + it.shift) : it.keys) : 0;  // keys the row sees

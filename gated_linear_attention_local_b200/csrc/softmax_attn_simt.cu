@@ -1,4 +1,4 @@
-// Softmax attention on the CUDA cores, for fp32 or bf16 operands: forward, dk / dv, dq and the row
+// Softmax attention on the CUDA cores, for fp32 operands: forward, dk / dv, dq and the row
 // sums delta.  64 x 64 tiles of scores, 256 threads, a 4 x 4 piece of the tile per thread
 // (rows 4 ty + i, columns tx + 16 j), fp32 FMA throughout.
 //
@@ -40,16 +40,10 @@ __device__ __forceinline__ int64_t row_offset(int64_t tok0, int64_t r, int G, in
 }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
 
 // rows [r0, r0 + 64) of one side into a tile, zeros past `rows` and past column D
-template <int DP, typename T>
-__device__ __forceinline__ void load_rows(float *tile, const T *src, int64_t tok0, int64_t r0, int64_t rows, int G,
+template <int DP>
+__device__ __forceinline__ void load_rows(float *tile, const float *src, int64_t tok0, int64_t r0, int64_t rows, int G,
                                           int H, int hk, int D) {
     constexpr int NV = DP / 4;
     for (int i = threadIdx.x; i < kB * NV; i += kThreads) {
@@ -116,7 +110,7 @@ __device__ __forceinline__ int64_t key_limit(const AttnArgs &a, const AttnTile &
     return a.causal ? min64(k_end, r / a.G + 1 + t.tk - t.tq) : k_end;
 }
 
-template <int DP, typename T>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, NC = DP / 16;
@@ -127,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t rows = t.tq * a.G;
     const int64_t kb = blockIdx.z * a.split, ke = min64(t.tk, kb + a.split);
-    load_rows<DP>(sq, static_cast<const T *>(a.q), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
+    load_rows<DP>(sq, static_cast<const float *>(a.q), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
     int64_t lim[4];
     int64_t last = 0;  // keys that some row of the tile sees
 #pragma unroll
@@ -144,8 +138,8 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
     const float sc = a.scale * kLog2e;
     for (int64_t j0 = kb; j0 < last; j0 += kB) {
         __syncthreads();
-        load_rows<DP>(sk, static_cast<const T *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
-        load_rows<DP>(sv, static_cast<const T *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+        load_rows<DP>(sk, static_cast<const float *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+        load_rows<DP>(sv, static_cast<const float *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
         __syncthreads();
         float s[4][4] = {};
         dot_rows<DP>(sq, sk, ty, tx, s);
@@ -199,13 +193,13 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnArgs a) {
             if (col >= a.D) continue;
             const float x = nan ? l[i] : o[i][c] * inv;
             if (a.part_o) a.part_o[pr * a.D + col] = x;
-            else static_cast<T *>(a.o)[row * a.D + col] = from_f32<T>(x);
+            else static_cast<float *>(a.o)[row * a.D + col] = x;
         }
     }
 }
 
 // One key tile (64 keys of one key head): dk, dv over every row that sees it.
-template <int DP, typename T>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_bwd_dkdv_simt_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, NC = DP / 16;
@@ -216,16 +210,16 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_dkdv_simt_kernel(AttnArgs a
     if (!attn_locate(a, false, blockIdx.x, 1, kB, t)) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t rows = t.tq * a.G, j0 = t.row0;
-    load_rows<DP>(sk, static_cast<const T *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
-    load_rows<DP>(sv, static_cast<const T *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+    load_rows<DP>(sk, static_cast<const float *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+    load_rows<DP>(sv, static_cast<const float *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
     // the first row that sees key j0
     const int64_t first = a.causal ? (j0 > t.tk - t.tq ? (j0 - (t.tk - t.tq)) * a.G : 0) : 0;
     float dk[4][NC] = {}, dv[4][NC] = {};
     const float sc = a.scale * kLog2e;
     for (int64_t r0 = first; r0 < rows; r0 += kB) {
         __syncthreads();
-        load_rows<DP>(sq, static_cast<const T *>(a.q), t.q0, r0, rows, a.G, a.H, hk, a.D);
-        load_rows<DP>(sd, static_cast<const T *>(a.dout), t.q0, r0, rows, a.G, a.H, hk, a.D);
+        load_rows<DP>(sq, static_cast<const float *>(a.q), t.q0, r0, rows, a.G, a.H, hk, a.D);
+        load_rows<DP>(sd, static_cast<const float *>(a.dout), t.q0, r0, rows, a.G, a.H, hk, a.D);
         if (threadIdx.x < kB) {
             const int64_t r = r0 + threadIdx.x;
             const int64_t row = r < rows ? row_offset(t.q0, r, a.G, a.H, hk) : 0;
@@ -262,14 +256,14 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_dkdv_simt_kernel(AttnArgs a
         for (int c = 0; c < NC; ++c) {
             const int col = 2 * tx + 32 * (c >> 1) + (c & 1);
             if (col >= a.D) continue;
-            static_cast<T *>(a.dk)[off + col] = from_f32<T>(dk[i][c] * a.scale);
-            static_cast<T *>(a.dv)[off + col] = from_f32<T>(dv[i][c]);
+            static_cast<float *>(a.dk)[off + col] = dk[i][c] * a.scale;
+            static_cast<float *>(a.dv)[off + col] = dv[i][c];
         }
     }
 }
 
 // One query tile: dq over every key its rows see.
-template <int DP, typename T>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_bwd_dq_simt_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, NC = DP / 16;
@@ -279,8 +273,8 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_dq_simt_kernel(AttnArgs a) 
     if (!attn_locate(a, true, blockIdx.x, a.G, kB, t)) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t rows = t.tq * a.G;
-    load_rows<DP>(sq, static_cast<const T *>(a.q), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
-    load_rows<DP>(sd, static_cast<const T *>(a.dout), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
+    load_rows<DP>(sq, static_cast<const float *>(a.q), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
+    load_rows<DP>(sd, static_cast<const float *>(a.dout), t.q0, t.row0, rows, a.G, a.H, hk, a.D);
     int64_t lim[4];
     float lse[4], delta[4];
 #pragma unroll
@@ -296,8 +290,8 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_dq_simt_kernel(AttnArgs a) 
     const float sc = a.scale * kLog2e;
     for (int64_t j0 = 0; j0 < last; j0 += kB) {
         __syncthreads();
-        load_rows<DP>(sk, static_cast<const T *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
-        load_rows<DP>(sv, static_cast<const T *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+        load_rows<DP>(sk, static_cast<const float *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
+        load_rows<DP>(sv, static_cast<const float *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
         __syncthreads();
         float s[4][4] = {}, dp[4][4] = {};
         dot_rows<DP>(sq, sk, ty, tx, s);
@@ -319,25 +313,21 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_dq_simt_kernel(AttnArgs a) 
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int col = 2 * tx + 32 * (c >> 1) + (c & 1);
-            if (col < a.D) static_cast<T *>(a.dq)[off + col] = from_f32<T>(dq[i][c] * a.scale);
+            if (col < a.D) static_cast<float *>(a.dq)[off + col] = dq[i][c] * a.scale;
         }
     }
 }
 
 // One warp a row (token, head): delta = sum_d do o.  HBM bound (reads do and o once).
-template <typename T>
-__global__ void attn_delta_kernel(const T *__restrict__ dout, const T *__restrict__ o, float *__restrict__ delta,
+__global__ void attn_delta_kernel(const float *__restrict__ dout, const float *__restrict__ o, float *__restrict__ delta,
                                   int64_t rows, int D) {
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t r = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
         float acc = 0.f;
-        for (int c = 4 * lane; c < D; c += 128) {  // D is a multiple of 8
-            T x[4], y[4];
-            memcpy(x, __builtin_assume_aligned(dout + r * D + c, 4 * sizeof(T)), sizeof(x));
-            memcpy(y, __builtin_assume_aligned(o + r * D + c, 4 * sizeof(T)), sizeof(y));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc = fmaf(to_f32(x[e]), to_f32(y[e]), acc);
+        if (4 * lane < D) {  // D is a multiple of 8, at most 128
+            const float4 x = load4(dout + r * D + 4 * lane), y = load4(o + r * D + 4 * lane);
+            acc = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
         }
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
@@ -360,48 +350,43 @@ cudaError_t launch(F kern, dim3 grid, size_t smem, const AttnArgs &a, cudaStream
 }
 
 // 0: forward, 1: dk dv, 2: dq
-template <int DP, typename T>
+template <int DP>
 cudaError_t launch_part(int part, const AttnArgs &a, cudaStream_t st) {
     const dim3 gq((unsigned)attn_slots(a.sq, a.N, a.G, kB), a.Hk, part == 0 ? a.nsplit : 1);
     const dim3 gk((unsigned)attn_slots(a.sk, a.N, 1, kB), a.Hk);
-    if (part == 0) return launch(attn_fwd_simt_kernel<DP, T>, gq, smem_bytes<DP>(3, 1), a, st);
-    if (part == 1) return launch(attn_bwd_dkdv_simt_kernel<DP, T>, gk, smem_bytes<DP>(4, 2), a, st);
-    return launch(attn_bwd_dq_simt_kernel<DP, T>, gq, smem_bytes<DP>(4, 1), a, st);
+    if (part == 0) return launch(attn_fwd_simt_kernel<DP>, gq, smem_bytes<DP>(3, 1), a, st);
+    if (part == 1) return launch(attn_bwd_dkdv_simt_kernel<DP>, gk, smem_bytes<DP>(4, 2), a, st);
+    return launch(attn_bwd_dq_simt_kernel<DP>, gq, smem_bytes<DP>(4, 1), a, st);
 }
 
 // column width of the tiles: D rounded up to a multiple of 32
-template <typename T>
 cudaError_t launch_width(int part, const AttnArgs &a, cudaStream_t st) {
     switch ((a.D + 31) / 32) {
-        case 1: return launch_part<32, T>(part, a, st);
-        case 2: return launch_part<64, T>(part, a, st);
-        case 3: return launch_part<96, T>(part, a, st);
-        default: return launch_part<128, T>(part, a, st);
+        case 1: return launch_part<32>(part, a, st);
+        case 2: return launch_part<64>(part, a, st);
+        case 3: return launch_part<96>(part, a, st);
+        default: return launch_part<128>(part, a, st);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st) {
-    return a.bf16 ? launch_width<__nv_bfloat16>(0, a, st) : launch_width<float>(0, a, st);
+    return launch_width(0, a, st);
 }
 cudaError_t launch_attn_bwd_dkdv_simt(const AttnArgs &a, cudaStream_t st) {
-    return a.bf16 ? launch_width<__nv_bfloat16>(1, a, st) : launch_width<float>(1, a, st);
+    return launch_width(1, a, st);
 }
 cudaError_t launch_attn_bwd_dq_simt(const AttnArgs &a, cudaStream_t st) {
-    return a.bf16 ? launch_width<__nv_bfloat16>(2, a, st) : launch_width<float>(2, a, st);
+    return launch_width(2, a, st);
 }
 
-cudaError_t launch_attn_delta(const AttnArgs &a, const void *o, cudaStream_t st) {
+cudaError_t launch_attn_delta(const AttnArgs &a, cudaStream_t st) {
     const int64_t rows = (a.sq.cu ? a.sq.T : a.N * a.sq.T) * a.H;
     if (rows == 0) return cudaSuccess;
     const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, 148 * 16);
-    if (a.bf16)
-        attn_delta_kernel<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(a.dout),
-                                                static_cast<const __nv_bfloat16 *>(o), a.delta, rows, a.D);
-    else
-        attn_delta_kernel<<<grid, 256, 0, st>>>(static_cast<const float *>(a.dout), static_cast<const float *>(o),
-                                                a.delta, rows, a.D);
+    attn_delta_kernel<<<grid, 256, 0, st>>>(static_cast<const float *>(a.dout), static_cast<const float *>(a.o), a.delta,
+                                            rows, a.D);
     return cudaGetLastError();
 }
 

@@ -31,5 +31,87 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
 }
 
 
+// Work items of a kernel whose grid has a block for every item but whose CTAs stay on their SM: a
+// scheduler warp takes over blocks that have not started (clusterlaunchcontrol), describes them
+// and hands the description to the other warps.  It asks when the copies of the item in work
+// have all been issued: early enough to hide the answer, late enough not to hold an item back
+// from SMs that run idle before (asking at the item's start instead: dk dv of 2 x 4096 tokens,
+// 1.7 items a CTA, 325 us for LATE us).  Item has int n, the tiles of the item; n < 0: no more.
+constexpr int kFeedWarps = 10;  // warps that take items: eight row warps, copies, products
+template <typename Item>
+struct Feed {
+    uint64_t *full, *empty, *want, *next;  // description written, taken, next one wanted, answer arrived
+    void *answer;                   // 16 bytes, 16-byte aligned
+    Item *item;
+    volatile int *abort_flag;
+
+    __device__ void init() const {
+        mbar_init(full, 1);
+        mbar_init(empty, kFeedWarps);
+        mbar_init(want, 1);
+        mbar_init(next, 1);
+    }
+    // The next item, by all lanes of a warp; false when there is none.
+    __device__ bool take(int &count, Item &it) const {
+        if (!mbar_wait(full, count & 1, abort_flag)) return false;
+        it = *item;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+        ++count;
+        return it.n >= 0;
+    }
+    // The scheduler warp: describe(u, it) fills the item of block u, false if it has nothing to do.
+    template <typename F>
+    __device__ void run(F describe) const {
+        const int lane = threadIdx.x & 31;
+        int count = 0;
+        bool ok = true;
+        auto publish = [&](const Item &it) {
+            if (count > 0) ok = mbar_wait_idle(empty, (count - 1) & 1, abort_flag);
+            __syncwarp();
+            if (ok && lane == 0) {
+                *item = it;
+                mbar_arrive(full);
+            }
+            __syncwarp();
+            ++count;
+        };
+        for (int u = blockIdx.x, asked = 0; ok && u >= 0;) {
+            Item it;
+            if (describe(u, it)) {
+                publish(it);
+                if (!ok || !(ok = mbar_wait_idle(want, (count - 1) & 1, abort_flag))) break;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                fence_proxy_async_smem();  // the last answer has been read
+                mbar_arrive_expect_tx(next, 16);
+                next_block_request(answer, next);
+            }
+            __syncwarp();
+            if (!(ok = mbar_wait(next, asked & 1, abort_flag))) break;
+            ++asked;
+            u = next_block_answer(answer);
+            __syncwarp();
+        }
+        Item end{};
+        end.n = -1;
+        if (ok) publish(end);
+    }
+};
+
+// A ring of N stages: the stage in turn and the parity of its use.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step() {
+        if (++s == N) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
 }  // namespace
 }  // namespace sgla
