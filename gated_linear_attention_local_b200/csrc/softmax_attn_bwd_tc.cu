@@ -107,7 +107,8 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int lan
 
 // Columns [0, D) of this thread's accumulator row times f, as bf16 to dst (zeros with !any; nullptr:
 // not stored).
-__device__ __forceinline__ void store_acc(uint32_t taddr, bool any, __nv_bfloat16 *dst, int D, float f) {
+__device__ __forceinline__ void store_acc(uint32_t taddr, bool any, __nv_bfloat16 *dst, int D, float f,
+                                          bool wide) {
     __syncwarp();
     for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -117,13 +118,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, bool any, __nv_bfloat1
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f : 0.f;
-        if (dst)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + 8 * e < D)
-                    *reinterpret_cast<uint4 *>(dst + c + 8 * e) =
-                        make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                   pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+        if (dst) store_cols32(dst + c, o, D - c, wide);
         __syncwarp();  // the next tensor memory read is the whole warp's
     }
 }
@@ -271,7 +266,7 @@ template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R,
-                    int slots) {
+                    int slots, bool wide) {
     using C = BwdCfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_bwd[];
     unsigned char *sm = smem_bwd;
@@ -370,50 +365,53 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             const int whole = it.q_left / R;  // tiles before the first partial one
             if (!(ok = wait(b.own, own_ph))) break;
             own_ph ^= 1u;
+            // two blocks of products a tile, each issued without a pause (the pipe holds few
+            // products, so a wait between two blocks is time it idles): dV(i) S(i+1), dK(i) dP(i+1)
             for (int i = -1; ok && i < n; ++i) {
-                if (i >= 0) {
-                    if (!(ok = wait(b.p, ph))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+                const bool more = i + 1 < n;
+                if (more) {
+                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                }
+                if (i >= 0 && !(ok = wait(b.p, ph))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (i >= 0) {
                         issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, y0.s * C::T), idA, i > 0);
                         mma_commit(&b.empty_y[y0.s]);
                     }
-                    __syncwarp();
-                    y0.step();
-                }
-                if (i + 1 < n) {
-                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
-                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
-                    tc_fence_after();
-                    if (elect_one()) {
+                    if (more) {
                         issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, x1.s * C::T), idS, nk);
                         mma_commit(b.s);
                     }
-                    __syncwarp();
-                    x1.step();
                 }
-                if (i >= 0) {
-                    if (!(ok = wait(&b.ds[0], ph))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, x0.s * C::T), idA, i > 0);
-                        mma_commit(&b.empty_x[x0.s]);
-                        if (i == n - 1) mma_commit(b.done);
-                    }
-                    __syncwarp();
-                    x0.step();
-                    ph ^= 1u;
-                }
-                if (i + 1 < n) {
+                __syncwarp();
+                if (more) {
                     if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
                     if (i + 1 >= whole) zero_rows<C::NG>(sm + C::Y0 + y1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
-                    tc_fence_after();
-                    if (elect_one()) {
+                }
+                if (i >= 0 && !(ok = wait(&b.ds[0], ph))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (i >= 0) {
+                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, x0.s * C::T), idA, i > 0);
+                        mma_commit(&b.empty_x[x0.s]);
+                        if (!more) mma_commit(b.done);
+                    }
+                    if (more) {
                         issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, y1.s * C::T), idS, nk);
                         mma_commit(&b.dp[0]);
                         if (i + 1 == n - 1) mma_commit(b.empty_own);
                     }
-                    __syncwarp();
+                }
+                __syncwarp();
+                if (i >= 0) {
+                    y0.step();
+                    x0.step();
+                    ph ^= 1u;
+                }
+                if (more) {
+                    x1.step();
                     y1.step();
                 }
             }
@@ -497,7 +495,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             __nv_bfloat16 *dst = r < it.k_left ? static_cast<__nv_bfloat16 *>(w == 0 ? a.dv : a.dk) +
                                                      ((int64_t)(it.k_tok + r) * a.Hk + it.hk) * a.D
                                                : nullptr;
-            store_acc(tmem + C::COL_ACC + w * 128 + lanes, n > 0, dst, a.D, w == 0 ? 1.f : a.scale);
+            store_acc(tmem + C::COL_ACC + w * 128 + lanes, n > 0, dst, a.D, w == 0 ? 1.f : a.scale, wide);
             tc_fence_before();  // the next item's first sums overwrite the accumulators after its P arrives
         }
         if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
@@ -528,7 +526,7 @@ template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, AttnArgs a, int R,
-                  int slots) {
+                  int slots, bool wide) {
     using C = BwdCfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_bwd[];
     unsigned char *sm = smem_bwd;
@@ -626,24 +624,20 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
                     const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
                     if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
+                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
                     if (!(ok = wait(b.sfree, free_ph))) break;  // (the very first passes at once)
                     free_ph ^= 1u;
                     tc_fence_after();
                     if (elect_one()) {
                         issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
                         mma_commit(b.s);
-                    }
-                    __syncwarp();
-                    x1.step();
-                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
                         issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
                         mma_commit(&b.dp[d1.s]);
                         mma_commit(&b.empty_y[y1.s]);
                         if (i + 1 == n - 1) mma_commit(b.empty_own);
                     }
                     __syncwarp();
+                    x1.step();
                     y1.step();
                     d1.step();
                 }
@@ -675,8 +669,6 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         const uint32_t cS = tmem + C::COL_S + lanes, cDP = tmem + C::COL_DP + lanes;
         const int tr = r / a.G, tg = r - tr * a.G;
         const float sc = a.scale * kLog2e;
-        // the 16-byte pieces of a row that this warpgroup takes for delta
-        const int pieces = a.D / 8, piece0 = w == 0 ? 0 : (pieces + 1) / 2, piece1 = w == 0 ? (pieces + 1) / 2 : pieces;
         QItem it;
         int ni = 0;
         uint32_t tile = 0, done_ph = 0;
@@ -688,29 +680,40 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const int lim = mine ? max(0, a.causal ? min(it.keys, tr + 1 + it.shift) : it.keys) : 0;
             const int64_t row = mine ? (int64_t)(it.q_tok + tr) * a.H + it.hk * a.G + tg : 0;
             const float lse = mine ? a.lse_in[row] * kLog2e : 0.f;
-            // delta = sum_d do o, half of the row in each warpgroup
-            float delta = 0.f;
-            if (mine) {
-                const uint4 *g4 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + row * a.D);
-                const uint4 *o4 = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + row * a.D);
+            // delta = sum_d do o: a lane takes a 16-byte piece of a row, a warp 16 rows
+            {
+                constexpr int PER = DP / 8, NK = 16 * PER / 32;
+                const int piece = lane & (PER - 1);
+                uint4 g[NK], o[NK];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (piece0 + e >= piece1) continue;
-                    const uint4 g = g4[piece0 + e], o = o4[piece0 + e];
-                    const uint32_t gs[4] = {g.x, g.y, g.z, g.w}, os[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gs[k]));
-                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&os[k]));
-                        delta = fmaf(x.x, y.x, delta);
-                        delta = fmaf(x.y, y.y, delta);
+                for (int k = 0; k < NK; ++k) {  // every load first
+                    const int rr = warp * 16 + k * (32 / PER) + lane / PER, t = rr / a.G;
+                    g[k] = o[k] = make_uint4(0, 0, 0, 0);
+                    if (t < R && t < it.q_left && 8 * piece < a.D) {
+                        const int64_t at = ((int64_t)(it.q_tok + t) * a.H + it.hk * a.G + rr - t * a.G) * a.D + 8 * piece;
+                        g[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.dout) + at);
+                        o[k] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + at);
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    const uint32_t gs[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, os[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+                    float x = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&gs[e]));
+                        const float2 z = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&os[e]));
+                        x = fmaf(y.x, z.x, x);
+                        x = fmaf(y.y, z.y, x);
+                    }
+#pragma unroll
+                    for (int d = PER / 2; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    // (the other half of srow belongs to the item before)
+                    if (piece == 0) srow[(ni & 1) * 256 + warp * 16 + k * (32 / PER) + lane / PER] = x;
+                }
             }
-            __syncwarp();
-            srow[(ni & 1) * 256 + threadIdx.x] = delta;  // (the other half belongs to the item before)
-            pair_sync(warp);
-            delta += srow[(ni & 1) * 256 + (threadIdx.x ^ 128)];
+            named_sync(1, 256);
+            float delta = srow[(ni & 1) * 256 + r];
             if (mine && w == 0) a.delta[row] = delta;
             // A wait that gave up skips the later ones but none of the barriers: no thread is left behind.
             for (int i = 0; i < n; ++i, ++tile) {
@@ -760,9 +763,9 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             if (!ok) continue;
             tc_fence_after();
             // each warpgroup stores half of the columns
-            const int h0 = w == 0 ? 0 : 64, h1 = w == 0 ? min(a.D, 64) : a.D;
+            const int half = a.D > 64 ? 64 : 32, h0 = w == 0 ? 0 : half, h1 = w == 0 ? min(a.D, half) : a.D;
             __nv_bfloat16 *dst = mine ? static_cast<__nv_bfloat16 *>(a.dq) + row * a.D + h0 : nullptr;
-            if (h1 > h0) store_acc(tmem + C::COL_ACC + 128 + h0 + lanes, n > 0, dst, h1 - h0, a.scale);
+            if (h1 > h0) store_acc(tmem + C::COL_ACC + 128 + h0 + lanes, n > 0, dst, h1 - h0, a.scale, wide);
             tc_fence_before();  // the next item's first sum overwrites the accumulator after its dS arrives
         }
         if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
@@ -808,7 +811,8 @@ cudaError_t launch_dkdv(const AttnArgs &a, const Maps &m, int R, cudaStream_t st
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a.sk, a.N, 1, kTile);
     if (slots * a.Hk >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots);
+    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots,
+                                                              wide_rows(a.dk, a.D) && wide_rows(a.dv, a.D));
     return cudaGetLastError();
 }
 
@@ -821,7 +825,8 @@ cudaError_t launch_dq(const AttnArgs &a, const Maps &m, int R, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a.sq, a.N, 1, R);
     if (slots * a.Hk >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots);
+    kern<<<(unsigned)(slots * a.Hk), kBwdThreads, smem, st>>>(m.q, m.dout, m.k, m.v, a, R, (int)slots,
+                                                              wide_rows(a.dq, a.D));
     return cudaGetLastError();
 }
 

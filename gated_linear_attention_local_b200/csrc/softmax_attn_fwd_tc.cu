@@ -105,7 +105,8 @@ __device__ __forceinline__ void probabilities(const float (&s)[32], float sc, fl
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, AttnArgs a, int R, int slots) {
+                   const __grid_constant__ CUtensorMap tv, AttnArgs a, int R, int slots,
+                   bool wide) {
     using C = FwdCfg<DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = align1024(smem_raw);
@@ -241,28 +242,29 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const int n = max(nt[0], nt[1]);
             for (int j = -1; ok && j < n; ++j) {
                 const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
-                bool vready = false, kready = false;
+                const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
+                if (j >= 0) {
+                    if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
+                    const int valid = it.k_left - j * kTile;
+                    if (valid < kTile) {
+                        // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
+                        for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
+                            const int r = (i >> 3) & (kTile - 1);
+                            if (r >= valid)
+                                *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion + r * 128 +
+                                                           (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (j + 1 < n && !(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
+                const bool second = j < 0 ? nt[1] > 0 : j < nt[1];  // row tile 1 has products here
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (!ok) break;
-                    if (j >= 0 && j < nt[w]) {
-                        const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T);
-                        if (!vready) {
-                            if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
-                            vready = true;
-                            const int valid = it.k_left - j * kTile;
-                            if (valid < kTile) {
-                                // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
-                                for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
-                                    const int r = (i >> 3) & (kTile - 1);
-                                    if (r >= valid)
-                                        *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion +
-                                                                   r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                                }
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                        }
+                    const bool pv = j >= 0 && j < nt[w], more = j + 1 < nt[w];
+                    if (pv) {
                         if (!(ok = wait(&b_pa[w], np[w] & 1))) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -273,29 +275,24 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         }
                         __syncwarp();
                         if (!(ok = wait(&b_pb[w], np[w] & 1))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
+                        ++np[w];
+                    }
+                    if (j < 0 && more) {
+                        if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
+                        ++nq[w];
+                    }
+                    tc_fence_after();
+                    // the rest of P V and the next scores without a pause: the pipe holds few products
+                    if ((pv || more) && elect_one()) {
+                        if (pv) {
 #pragma unroll
                             for (int jj = 6; jj < 8; ++jj)
                                 mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
                                                 desc_at(v0, jj * 2048), idO, 1u);
-                            if (j == nt[w] - 1) mma_commit(&b_o[w]);
+                            if (!more) mma_commit(&b_o[w]);
                         }
-                        ++np[w];
-                        __syncwarp();
-                    }
-                    if (j + 1 < nt[w]) {
-                        if (j < 0) {
-                            if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
-                            ++nq[w];
-                        }
-                        if (!kready) {
-                            if (!(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
-                            kready = true;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint64_t q1 = desc_at(qd, w * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
+                        if (more) {
+                            const uint64_t q1 = desc_at(qd, w * C::T);
 #pragma unroll
                             for (int kk = 0; kk < DP / 16; ++kk)
                                 if (kk < nk)
@@ -304,14 +301,13 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             mma_commit(&b_s[w]);
                             if (j + 1 == nt[w] - 1) mma_commit(&empty_q[w]);
                         }
-                        __syncwarp();
+                        if (w == 1 || !second) {  // the last products of this pair of tiles
+                            if (j >= 0) mma_commit(&empty_v[c0 & 1]);
+                            if (j + 1 < n) mma_commit(&empty_k[c1 & 1]);
+                        }
                     }
+                    __syncwarp();
                 }
-                if (ok && elect_one()) {
-                    if (j >= 0) mma_commit(&empty_v[c0 & 1]);
-                    if (j + 1 < n) mma_commit(&empty_k[c1 & 1]);
-                }
-                __syncwarp();
             }
             kv += n;
         }
@@ -432,13 +428,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         if (c + 4 * e < a.D)
                             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else if (mine) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row * a.D + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + 8 * e < a.D)
-                            dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                                                pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                    store_cols32(static_cast<__nv_bfloat16 *>(a.o) + row * a.D + c, o, a.D - c, wide);
                 }
                 __syncwarp();  // the next tensor memory read is the whole warp's
             }
@@ -467,7 +457,7 @@ cudaError_t launch_fwd(const AttnArgs &a, const CUtensorMap &tq, const CUtensorM
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a.sq, a.N, 1, 2 * R), items = slots * a.Hk * a.nsplit;
     if (items >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-    kern<<<(unsigned)items, kFwdThreads, smem, st>>>(tq, tk, tv, a, R, (int)slots);
+    kern<<<(unsigned)items, kFwdThreads, smem, st>>>(tq, tk, tv, a, R, (int)slots, wide_rows(a.o, a.D));
     return cudaGetLastError();
 }
 

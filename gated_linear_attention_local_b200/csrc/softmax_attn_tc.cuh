@@ -31,12 +31,36 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
 }
 
 
+// 32 columns of an output row, the first `left` of them (a multiple of 8), as bf16 to dst.  Every
+// lane of a warp stores another row, so an instruction touches 32 lines whatever its width: 32
+// bytes at a time where rows are aligned to that (`wide`), else 16.
+__device__ __forceinline__ void store_cols32(__nv_bfloat16 *dst, const float (&o)[32], int left, bool wide) {
+    uint32_t u[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) u[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
+    if (wide) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (16 * e < left) {
+                const uint32_t v[8] = {u[8 * e], u[8 * e + 1], u[8 * e + 2], u[8 * e + 3],
+                                       u[8 * e + 4], u[8 * e + 5], u[8 * e + 6], u[8 * e + 7]};
+                st_global_v8(dst + 16 * e, v);
+            }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (8 * e < left)
+                *reinterpret_cast<uint4 *>(dst + 8 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+    }
+}
+inline bool wide_rows(const void *p, int D) { return D % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
 // Work items of a kernel whose grid has a block for every item but whose CTAs stay on their SM: a
 // scheduler warp takes over blocks that have not started (clusterlaunchcontrol), describes them
 // and hands the description to the other warps.  It asks when the copies of the item in work
 // have all been issued: early enough to hide the answer, late enough not to hold an item back
 // from SMs that run idle before (asking at the item's start instead: dk dv of 2 x 4096 tokens,
-// 1.7 items a CTA, 325 us for LATE us).  Item has int n, the tiles of the item; n < 0: no more.
+// 1.7 items a CTA, 325 us for 229 us).  Item has int n, the tiles of the item; n < 0: no more.
 constexpr int kFeedWarps = 10;  // warps that take items: eight row warps, copies, products
 template <typename Item>
 struct Feed {
