@@ -14,11 +14,11 @@
 //
 // Bound: HBM (each element read and written once).  cos and sin depend on the token and the
 // pair only, so a block first forms those of its tokens once (shared memory) and then streams
-// every head of q and k past them in 16-byte vectors, an item (two vectors) a thread at a time:
-// small threads and blocks of 128 keep enough of them on an SM to cover the latency.  65536
-// tokens of 32 + 8 heads of 128 (1.34 GB): 215 us, 95 % of the measured copy rate (two items a
-// thread 248 us, four 388 us; blocks of 256 224 us).
+// every head of q and k past them in 16-byte vectors, an item (two vectors) a thread at a time
+// (two or four items in flight measured slower, 248 and 388 us).  65536 tokens of 32 + 8 heads of
+// 128 (1.34 GB): 214 us, 96 % of the measured copy rate.
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -48,9 +48,32 @@ struct alignas(sizeof(T) * VEC) Vec {
     T x[VEC];
 };
 
+// STREAM: 16-byte vectors bypass the L2's replacement order (evict first).
+template <bool STREAM, typename V>
+__device__ __forceinline__ V load_vec(const void *p) {
+    if constexpr (STREAM && sizeof(V) == 16) {
+        const uint4 u = __ldcs(static_cast<const uint4 *>(p));
+        V v;
+        memcpy(&v, &u, 16);
+        return v;
+    } else {
+        return *static_cast<const V *>(p);
+    }
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_vec(void *p, const V &v) {
+    if constexpr (STREAM && sizeof(V) == 16) {
+        uint4 u;
+        memcpy(&u, &v, 16);
+        __stcs(static_cast<uint4 *>(p), u);
+    } else {
+        *static_cast<V *>(p) = v;
+    }
+}
+
 // Items of one head: half layout R/2/VEC items of two vectors (the pairs' first and second
 // elements), interleaved R/VEC items of one vector; then (D-R)/VEC vectors that are copied.
-template <typename T, int VEC, bool INTER>
+template <typename T, int VEC, bool INTER, bool STREAM>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
     // [tpb][half] cos, sin.  PV pairs belong to an item; they lie two by two, [PV / 2][items][2],
     // so that the lanes of consecutive items read consecutive 16 bytes.
@@ -79,9 +102,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         const int64_t off = (isq ? (t0 + tok) * a.H + h : (t0 + tok) * a.Hk + (h - a.H)) * a.D + col;
         const T *src = static_cast<const T *>(isq ? a.q : a.k) + off;
         T *dst = static_cast<T *>(isq ? a.qo : a.ko) + off;
-        V x = *reinterpret_cast<const V *>(src), y;
+        V x = load_vec<STREAM, V>(src), y;
         if (rotates) {
-            if constexpr (!INTER) y = *reinterpret_cast<const V *>(src + a.half);
+            if constexpr (!INTER) y = load_vec<STREAM, V>(src + a.half);
             float2 w[PV];
 #pragma unroll
             for (int e = 0; e < PV; e += PQ) {
@@ -108,24 +131,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
                     x.x[e] = from_f32<T>(p * w[e].x - s * w[e].y);
                     y.x[e] = from_f32<T>(p * w[e].y + s * w[e].x);
                 }
-                *reinterpret_cast<V *>(dst + a.half) = y;
+                store_vec<STREAM>(dst + a.half, y);
             }
         }
-        *reinterpret_cast<V *>(dst) = x;
+        store_vec<STREAM>(dst, x);
     }
 }
 
-template <typename T, int VEC>
-cudaError_t launch_rotary(const RotArgs &a, bool inter, cudaStream_t st) {
+template <typename T, int VEC, bool INTER>
+cudaError_t launch_rotary(const RotArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.tokens + a.tpb - 1) / a.tpb);
     const size_t smem = (size_t)a.tpb * a.half * sizeof(float2);
-    if constexpr (VEC >= 2) {
-        if (inter) {
-            rotary_kernel<T, VEC, true><<<grid, kRotThreads, smem, st>>>(a);
-            return cudaGetLastError();
-        }
-    }
-    rotary_kernel<T, VEC, false><<<grid, kRotThreads, smem, st>>>(a);
+    // Tensors that pass twice the L2 (126 MB) gain from the streaming hints (264 -> 214 us at
+    // 1.34 GB); smaller ones stay for the kernel that reads them next (36.7 us with, 35.3 without
+    // at 168 MB).
+    if (2 * a.tokens * (a.H + a.Hk) * a.D * (int64_t)sizeof(T) > ((int64_t)252 << 20))
+        rotary_kernel<T, VEC, INTER, true><<<grid, kRotThreads, smem, st>>>(a);
+    else
+        rotary_kernel<T, VEC, INTER, false><<<grid, kRotThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -134,10 +157,11 @@ cudaError_t launch_rotary(const RotArgs &a, bool inter, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_rotary_vec(const RotArgs &a, bool inter, cudaStream_t st) {
     const int run = inter ? (a.D | (2 * a.half)) : (a.D | a.half);  // common low bits of the column offsets
-    if (sizeof(T) == 2 && run % 8 == 0) return launch_rotary<T, 16 / (int)sizeof(T)>(a, inter, st);
-    if (run % 4 == 0) return launch_rotary<T, 4>(a, inter, st);
-    if (run % 2 == 0) return launch_rotary<T, 2>(a, inter, st);
-    return launch_rotary<T, 1>(a, false, st);
+    constexpr int W = 16 / (int)sizeof(T);
+    if (run % W == 0) return inter ? launch_rotary<T, W, true>(a, st) : launch_rotary<T, W, false>(a, st);
+    if (W > 4 && run % 4 == 0) return inter ? launch_rotary<T, 4, true>(a, st) : launch_rotary<T, 4, false>(a, st);
+    if (run % 2 == 0) return inter ? launch_rotary<T, 2, true>(a, st) : launch_rotary<T, 2, false>(a, st);
+    return launch_rotary<T, 1, false>(a, st);
 }
 
 }  // namespace
