@@ -52,10 +52,10 @@ struct AttnArgs {
     void *dq, *dk, *dv;
 };
 
-// CUDA cores, fp32
-cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t st);
-cudaError_t launch_attn_bwd_dkdv_simt(const AttnArgs &a, cudaStream_t st);
-cudaError_t launch_attn_bwd_dq_simt(const AttnArgs &a, cudaStream_t st);
+// fp32 (three tf32 products for one)
+cudaError_t launch_attn_fwd_tf32(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dkdv_tf32(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_bwd_dq_tf32(const AttnArgs &a, cudaStream_t st);
 // delta_i = sum_d do_id o_id, one value a row (fp32)
 cudaError_t launch_attn_delta(const AttnArgs &a, cudaStream_t st);
 

@@ -67,7 +67,7 @@ sgla_status check_seqs(AttnArgs &a, const int64_t *cu_q, const int64_t *cu_k, in
 }
 
 cudaError_t launch_fwd(const AttnArgs &a, cudaStream_t st) {
-    return a.bf16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_simt(a, st);
+    return a.bf16 ? launch_attn_fwd_tc(a, st) : launch_attn_fwd_tf32(a, st);
 }
 
 // The one-token step.  Up to kDecodeMaxGroup query heads a key head the streaming kernel takes
@@ -186,10 +186,10 @@ sgla_status softmax_attention_bwd(const void *q, const void *k, const void *v, c
     if (q_tokens > 0 && !a.bf16) ATTN_LAUNCH("softmax_attention_delta", launch_attn_delta(a, st));
     // dq first: for bf16 it forms delta as well
     if (q_tokens > 0)
-        ATTN_LAUNCH("softmax_attention_dq", a.bf16 ? launch_attn_bwd_dq_tc(a, st) : launch_attn_bwd_dq_simt(a, st));
+        ATTN_LAUNCH("softmax_attention_dq", a.bf16 ? launch_attn_bwd_dq_tc(a, st) : launch_attn_bwd_dq_tf32(a, st));
     if (k_tokens > 0)
         ATTN_LAUNCH("softmax_attention_dkdv",
-                    a.bf16 ? launch_attn_bwd_dkdv_tc(a, st) : launch_attn_bwd_dkdv_simt(a, st));
+                    a.bf16 ? launch_attn_bwd_dkdv_tc(a, st) : launch_attn_bwd_dkdv_tf32(a, st));
     return SGLA_OK;
 }
 
