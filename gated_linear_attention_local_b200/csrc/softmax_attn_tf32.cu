@@ -16,9 +16,15 @@
 // in two passes, one per output side, so that every sum has one owner and one order; there the
 // two halves are partial sums, joined at the end.
 //
+// A cluster of up to 8 CTAs shares a tile where there are fewer tiles than SMs: each takes a part
+// of the keys (dk dv: of the rows), and the parts are joined through distributed shared memory
+// in a fixed order (2 x 317 queries and 501 keys, 8 heads on 4: 203 -> 144 us a training pass, with two
+// CTAs an SM up to D = 64).
+//
 // The scores' accumulators are the next product's A operand as they stand: columns 2 t and
 // 2 t + 1 of an accumulator are taken as k = t and k = t + 4, and the B operand's rows are read in
 // that order.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
@@ -26,9 +32,13 @@
 #include "softmax_attn.h"
 
 namespace sgla {
+
+namespace cg = cooperative_groups;
+
 namespace {
 
 constexpr int kB = 64;  // tile edge
+constexpr int kMaxCluster = 8;
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -183,20 +193,55 @@ __device__ __forceinline__ void put_acc(float *tile, const float (&o)[DP / 8][4]
     }
 }
 
+// This CTA's part [beg, end) of `tiles` tiles, cut evenly over its cluster.
+struct Part {
+    int rank, cs;
+    int64_t beg, end;
+    __device__ Part(int64_t tiles) {
+        const cg::cluster_group cluster = cg::this_cluster();
+        cs = (int)cluster.num_blocks();
+        rank = (int)cluster.block_rank();
+        const int64_t per = (tiles + cs - 1) / cs;
+        beg = rank * per;
+        end = min64(tiles, beg + per);
+    }
+};
+__device__ __forceinline__ void cluster_meet(int cs) {
+    if (cs > 1) cg::this_cluster().sync();
+    else __syncthreads();
+}
+// Sum over the cluster of the 4 floats at p of everyone's shared memory, in rank order.
+__device__ __forceinline__ float4 cluster_sum(float *p, int cs) {
+    const cg::cluster_group cluster = cg::this_cluster();
+    float4 x[kMaxCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < cs) x[r] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(p, r));
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+        if (r < cs) y = make_float4(y.x + x[r].x, y.y + x[r].y, y.z + x[r].z, y.w + x[r].w);
+    return y;
+}
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_fwd_tf32_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_fwd_tf32_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, T = kB * S;
     float *sq = sm, *skv = sq + T;                 // two stages of K, V
     float *sml = skv + 4 * T;                      // [2][64][2] maximum and sum of the halves
+    float *sall = sml + 4 * kB;                    // [64][2] of both
+    float *sw = sall + 2 * kB;                     // [8][64] weights of the cluster's parts, [64] 1 / sum
     AttnTile t;
     const int hk = blockIdx.y;
-    if (!attn_locate(a, true, blockIdx.x, a.G, kB, t)) return;
+    if (!attn_locate(a, true, blockIdx.x / cg::this_cluster().num_blocks(), a.G, kB, t)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp & 3, wc = warp >> 2;
     const int64_t rows = t.tq * a.G;
-    const int64_t kb = blockIdx.z * a.split, ke = min64(t.tk, kb + a.split);
+    const int64_t kb0 = blockIdx.z * a.split, ke = min64(t.tk, kb0 + a.split);
     const int nk = (a.D + 7) / 8;
-    const int64_t last = key_limit(a, t, min64(t.row0 + kB, rows) - 1, ke);  // keys that some row of the tile sees
+    // keys that some row of the tile sees, and this CTA's part of them
+    const int64_t seen = key_limit(a, t, min64(t.row0 + kB, rows) - 1, ke);
+    const Part part(seen > kb0 ? (seen - kb0 + kB - 1) / kB : 0);
+    const int64_t kb = kb0 + part.beg * kB, last = min64(seen, kb0 + part.end * kB);
     int64_t lim[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) lim[h] = key_limit(a, t, t.row0 + 16 * wr + 8 * h + (lane >> 2), ke);
@@ -258,8 +303,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_tf32_kernel(AttnArgs a) {
         __syncthreads();  // the stage may be filled again
     }
     copies_wait<0>();
-    // the two halves of the keys
-    float f[2];
+    // the two halves of the keys: their common maximum, the sum, o relative to that maximum
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -271,43 +315,70 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_tf32_kernel(AttnArgs a) {
         }
     }
     __syncthreads();
+    float f[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = 16 * wr + 8 * h + (lane >> 2);
-        const float m0 = sml[2 * r], m1 = sml[2 * (kB + r)], l0 = sml[2 * r + 1], l1 = sml[2 * (kB + r) + 1];
+        const float m0 = sml[2 * r], m1 = sml[2 * (kB + r)];
         const float top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
-        const float sum = l0 * exp2f(m0 - base) + l1 * exp2f(m1 - base);
-        f[h] = exp2f(m[h] - base) * (sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum));  // NaN scores stay NaN
-        const int64_t row = t.row0 + r;
-        if (wc == 0 && (lane & 3) == 0 && row < rows) {
+        f[h] = exp2f(m[h] - base);
+        if (wc == 0 && (lane & 3) == 0) {
+            sall[2 * r] = top;
+            sall[2 * r + 1] = sml[2 * r + 1] * exp2f(m0 - base) + sml[2 * (kB + r) + 1] * exp2f(m1 - base);
+        }
+    }
+    if (wc == 1) put_acc<DP>(sq, o, 16 * wr, f[0], f[1], false, lane);
+    __syncthreads();
+    if (wc == 0) put_acc<DP>(sq, o, 16 * wr, f[0], f[1], true, lane);
+    cluster_meet(part.cs);
+    // the parts of the cluster
+    const cg::cluster_group cluster = cg::this_cluster();
+    if (threadIdx.x < kB) {
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < part.cs; ++c) top = fmaxf(top, cluster.map_shared_rank(sall, c)[2 * threadIdx.x]);
+        const float base = top == -INFINITY ? 0.f : top;
+        for (int c = 0; c < part.cs; ++c) {
+            const float *p = cluster.map_shared_rank(sall, c) + 2 * threadIdx.x;
+            const float w = exp2f(p[0] - base);
+            sw[c * kB + threadIdx.x] = w;
+            sum = fmaf(w, p[1], sum);
+        }
+        sw[kMaxCluster * kB + threadIdx.x] = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN scores stay NaN
+        const int64_t row = t.row0 + threadIdx.x;
+        if (part.rank == 0 && row < rows) {
             const float lse = sum > 0.f ? (base + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
             const int64_t at = row_offset(t.q0, row, a.G, a.H, hk);
             if (a.part_lse) a.part_lse[blockIdx.z * a.part_rows + at] = lse;
             else if (a.lse) a.lse[at] = lse;
         }
     }
-    if (wc == 1) put_acc<DP>(sq, o, 16 * wr, f[0], f[1], false, lane);
     __syncthreads();
-    if (wc == 0) put_acc<DP>(sq, o, 16 * wr, f[0], f[1], true, lane);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kB * (DP / 4); i += kThreads) {
+    for (int i = part.rank * kThreads + threadIdx.x; i < kB * (DP / 4); i += part.cs * kThreads) {
         const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
         if (t.row0 + r >= rows || c >= a.D) continue;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < part.cs; ++p) {
+            const float4 y = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(sq, p) + r * S + c);
+            const float w = sw[p * kB + r];
+            x = make_float4(fmaf(w, y.x, x.x), fmaf(w, y.y, x.y), fmaf(w, y.z, x.z), fmaf(w, y.w, x.w));
+        }
+        const float inv = sw[kMaxCluster * kB + r];
         const int64_t at = row_offset(t.q0, t.row0 + r, a.G, a.H, hk);
         float *dst = a.part_o ? a.part_o + (blockIdx.z * a.part_rows + at) * a.D : static_cast<float *>(a.o) + at * a.D;
-        *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(sq + r * S + c);
+        *reinterpret_cast<float4 *>(dst + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     }
+    cluster_meet(part.cs);  // everyone's shared memory has been read
 }
 
 // 64 keys of one key head: dk, dv over every row that sees them.
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_dkdv_tf32_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_dkdv_tf32_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, T = kB * S;
     float *sk = sm, *sv = sk + T, *sq = sv + T, *sd = sq + T, *srow = sd + T;  // srow: [64] lse (log2 units), [64] delta
     AttnTile t;
     const int hk = blockIdx.y;
-    if (!attn_locate(a, false, blockIdx.x, 1, kB, t)) return;
+    if (!attn_locate(a, false, blockIdx.x / cg::this_cluster().num_blocks(), 1, kB, t)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp & 3, wc = warp >> 2;
     const int64_t rows = t.tq * a.G, j0 = t.row0;
     const int nk = (a.D + 7) / 8;
@@ -315,13 +386,15 @@ __global__ void __launch_bounds__(kThreads) attn_dkdv_tf32_kernel(AttnArgs a) {
     copy_rows<DP>(sv, static_cast<const float *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
     // the first row that sees key j0
     const int64_t first = a.causal ? (j0 > t.tk - t.tq ? (j0 - (t.tk - t.tq)) * a.G : 0) : 0;
+    const Part part(first < rows ? (rows - first + kB - 1) / kB : 0);
     float dk[DP / 8][4], dv[DP / 8][4];
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dk[n][e] = dv[n][e] = 0.f;
     const float sc = a.scale * kLog2e;
-    for (int64_t r0 = first; r0 < rows; r0 += kB) {
+    for (int64_t i = part.beg; i < part.end; ++i) {
+        const int64_t r0 = first + i * kB;
         __syncthreads();
         copy_rows<DP>(sq, static_cast<const float *>(a.q), t.q0, r0, rows, a.G, a.H, hk, a.D);
         copy_rows<DP>(sd, static_cast<const float *>(a.dout), t.q0, r0, rows, a.G, a.H, hk, a.D);
@@ -369,25 +442,26 @@ __global__ void __launch_bounds__(kThreads) attn_dkdv_tf32_kernel(AttnArgs a) {
         put_acc<DP>(sq, dk, 16 * wr, a.scale, a.scale, true, lane);
         put_acc<DP>(sd, dv, 16 * wr, 1.f, 1.f, true, lane);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kB * (DP / 4); i += kThreads) {
+    cluster_meet(part.cs);
+    for (int i = part.rank * kThreads + threadIdx.x; i < kB * (DP / 4); i += part.cs * kThreads) {
         const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
         if (j0 + r >= t.tk || c >= a.D) continue;
         const int64_t off = ((t.k0 + j0 + r) * a.Hk + hk) * a.D + c;
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.dk) + off) = *reinterpret_cast<const float4 *>(sq + r * S + c);
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.dv) + off) = *reinterpret_cast<const float4 *>(sd + r * S + c);
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.dk) + off) = cluster_sum(sq + r * S + c, part.cs);
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.dv) + off) = cluster_sum(sd + r * S + c, part.cs);
     }
+    cluster_meet(part.cs);  // everyone's shared memory has been read
 }
 
 // 64 packed rows: dq over every key they see.
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_dq_tf32_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_dq_tf32_kernel(AttnArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int S = Stride<DP>::value, T = kB * S;
     float *sq = sm, *sd = sq + T, *sk = sd + T, *sv = sk + T;
     AttnTile t;
     const int hk = blockIdx.y;
-    if (!attn_locate(a, true, blockIdx.x, a.G, kB, t)) return;
+    if (!attn_locate(a, true, blockIdx.x / cg::this_cluster().num_blocks(), a.G, kB, t)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp & 3, wc = warp >> 2;
     const int64_t rows = t.tq * a.G;
     const int nk = (a.D + 7) / 8;
@@ -403,14 +477,15 @@ __global__ void __launch_bounds__(kThreads) attn_dq_tf32_kernel(AttnArgs a) {
         lse[h] = r < rows ? a.lse_in[at] * kLog2e : 0.f;
         delta[h] = r < rows ? a.delta[at] : 0.f;
     }
-    const int64_t last = key_limit(a, t, min64(t.row0 + kB, rows) - 1, t.tk);
+    const int64_t seen = key_limit(a, t, min64(t.row0 + kB, rows) - 1, t.tk);
+    const Part part(seen > 0 ? (seen + kB - 1) / kB : 0);
     float dq[DP / 8][4];
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) dq[n][e] = 0.f;
     const float sc = a.scale * kLog2e;
-    for (int64_t j0 = 0; j0 < last; j0 += kB) {
+    for (int64_t j0 = part.beg * kB; j0 < part.end * kB; j0 += kB) {
         __syncthreads();
         copy_rows<DP>(sk, static_cast<const float *>(a.k), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
         copy_rows<DP>(sv, static_cast<const float *>(a.v), t.k0, j0, t.tk, 1, a.Hk, hk, a.D);
@@ -438,13 +513,14 @@ __global__ void __launch_bounds__(kThreads) attn_dq_tf32_kernel(AttnArgs a) {
     if (wc == 1) put_acc<DP>(sq, dq, 16 * wr, a.scale, a.scale, false, lane);
     __syncthreads();
     if (wc == 0) put_acc<DP>(sq, dq, 16 * wr, a.scale, a.scale, true, lane);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kB * (DP / 4); i += kThreads) {
+    cluster_meet(part.cs);
+    for (int i = part.rank * kThreads + threadIdx.x; i < kB * (DP / 4); i += part.cs * kThreads) {
         const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
         if (t.row0 + r >= rows || c >= a.D) continue;
         *reinterpret_cast<float4 *>(static_cast<float *>(a.dq) + row_offset(t.q0, t.row0 + r, a.G, a.H, hk) * a.D + c) =
-            *reinterpret_cast<const float4 *>(sq + r * S + c);
+            cluster_sum(sq + r * S + c, part.cs);
     }
+    cluster_meet(part.cs);  // everyone's shared memory has been read
 }
 
 // One warp a row (token, head): delta = sum_d do o.  HBM bound (reads do and o once).
@@ -465,13 +541,32 @@ __global__ void attn_delta_kernel(const float *__restrict__ dout, const float *_
     }
 }
 
+// CTAs a tile: as many as leave every SM at most two, and each at least two tiles of the other
+// side (`other` rows or keys, on average).
+int cluster_size(int64_t ctas, int64_t other) {
+    int cs = 1;
+    while (cs < kMaxCluster && ctas * cs * 2 <= 2 * 148 && other >= 4 * kB * cs) cs *= 2;
+    return cs;
+}
+
 template <typename F>
-cudaError_t launch(F kern, dim3 grid, size_t smem, const AttnArgs &a, cudaStream_t st, std::atomic<uint64_t> &done) {
+cudaError_t launch(F kern, dim3 grid, int cs, size_t smem, const AttnArgs &a, cudaStream_t st,
+                   std::atomic<uint64_t> &done) {
     if (grid.x == 0) return cudaSuccess;
     const cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid.x * cs, grid.y, grid.z);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // 0: forward, 1: dk dv, 2: dq
@@ -479,11 +574,16 @@ template <int DP>
 cudaError_t launch_part(int part, const AttnArgs &a, cudaStream_t st) {
     static std::atomic<uint64_t> done[3];
     const size_t tile = (size_t)kB * Stride<DP>::value;
-    const dim3 gq((unsigned)attn_slots(a.sq, a.N, a.G, kB), a.Hk, part == 0 ? a.nsplit : 1);
-    const dim3 gk((unsigned)attn_slots(a.sk, a.N, 1, kB), a.Hk);
-    if (part == 0) return launch(attn_fwd_tf32_kernel<DP>, gq, sizeof(float) * (5 * tile + 4 * kB), a, st, done[0]);
-    if (part == 1) return launch(attn_dkdv_tf32_kernel<DP>, gk, sizeof(float) * (4 * tile + 2 * kB), a, st, done[1]);
-    return launch(attn_dq_tf32_kernel<DP>, gq, sizeof(float) * 4 * tile, a, st, done[2]);
+    const int64_t nq = attn_slots(a.sq, a.N, a.G, kB), nk = attn_slots(a.sk, a.N, 1, kB);
+    const int64_t rows = (a.sq.cu ? a.sq.T / a.N : a.sq.T) * a.G, keys = a.sk.cu ? a.sk.T / a.N : a.sk.T;
+    const dim3 gq((unsigned)nq, a.Hk, part == 0 ? a.nsplit : 1), gk((unsigned)nk, a.Hk);
+    if (part == 0)
+        return launch(attn_fwd_tf32_kernel<DP>, gq, cluster_size(nq * a.Hk * a.nsplit, std::min(keys, a.split)),
+                      sizeof(float) * (5 * tile + (4 + 2 + kMaxCluster + 1) * kB), a, st, done[0]);
+    if (part == 1)
+        return launch(attn_dkdv_tf32_kernel<DP>, gk, cluster_size(nk * a.Hk, rows), sizeof(float) * (4 * tile + 2 * kB), a,
+                      st, done[1]);
+    return launch(attn_dq_tf32_kernel<DP>, gq, cluster_size(nq * a.Hk, keys), sizeof(float) * 4 * tile, a, st, done[2]);
 }
 
 // column width of the tiles: D rounded up to a multiple of 32
