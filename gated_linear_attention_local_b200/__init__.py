@@ -63,7 +63,7 @@ def _ptr(t):
 
 
 def _stream():
-    # the current stream's handle without a Stream object (0.1 us instead of 3.4 us a call)
+    # the current stream's handle without a Stream object (0.4 us instead of 3.4 us a call)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
@@ -73,15 +73,19 @@ def _on_tensor_device(fn):
     stream, so a call whose tensors live on another device than the current one
     switches to theirs first; tensors on two different devices are an error (the
     kernels read only memory local to the device they run on)."""
+    tensor = torch.Tensor
+
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         dev = None
-        for t in (*args, *kwargs.values()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                if dev is None:
-                    dev = t.device
-                elif t.device != dev:
-                    raise ValueError(f"{fn.__name__}: tensors on {dev} and {t.device}; all must be on one device")
+        for group in (args, kwargs.values()):
+            for t in group:
+                if isinstance(t, tensor) and t.is_cuda:
+                    d = t.device
+                    if dev is None:
+                        dev = d
+                    elif d != dev:
+                        raise ValueError(f"{fn.__name__}: tensors on {dev} and {d}; all must be on one device")
         if dev is None or dev.index == torch.cuda.current_device():
             return fn(*args, **kwargs)
         with torch.cuda.device(dev):

@@ -16,10 +16,18 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _DTYPES, _check_cuda, _on_tensor_device, _ptr, _scale, _stream, _workspace
-from ._lib import lib, raise_for_status
+from ._lib import SGLA_ERR_WORKSPACE, lib, raise_for_status
 
 __all__ = ["softmax_attention", "softmax_attention_fwd", "softmax_attention_bwd", "softmax_attention_decode_step",
            "SoftmaxAttentionFunction", "multi_axis_rotary", "multi_axis_rotary_bwd", "MultiAxisRotaryFunction"]
+
+
+def _check(name, t, dtype, ndim=None):
+    """_check_cuda, the usual case (nothing wrong) in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        _check_cuda(name, t, dtype)
+    if ndim is not None and t.dim() != ndim:
+        _check_cuda(name, t, dtype, ndim)
 
 
 def _operands(named):
@@ -30,8 +38,8 @@ def _operands(named):
     if dtype not in _DTYPES:
         raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
     for other, t in named[1:]:
-        _check_cuda(other, t)
-        if t.dtype != dtype:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+            _check_cuda(other, t)
             raise TypeError(f"{other} must be {dtype} like {name}, got {t.dtype}")
     return _DTYPES[dtype]
 
@@ -46,7 +54,7 @@ def _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k):
             raise ValueError("q must be [B,T,H,D] and k, v [B,S,Hk,D]")
         N = q.shape[0]
     else:
-        _check_cuda("cu_seqlens", cu_seqlens, torch.int64, 1)
+        _check("cu_seqlens", cu_seqlens, torch.int64, 1)
         _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int64, 1)
         if q.dim() not in (3, 4) or k.dim() != q.dim():
             raise ValueError("with cu_seqlens q must be [T,H,D] or [1,T,H,D], and k, v alike")
@@ -166,7 +174,7 @@ def softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, p
         raise ValueError(f"k_cache must be [{N},S,Hk,{D}], got {tuple(k_cache.shape)}")
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {H} query heads must be a multiple of the {Hk} key heads")
-    _check_cuda("lengths", lengths, torch.int64, 1)
+    _check("lengths", lengths, torch.int64, 1)
     if lengths.shape[0] != N:
         raise ValueError(f"lengths must be [{N}], got {tuple(lengths.shape)}")
     P = 0
@@ -187,45 +195,57 @@ def softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, p
         _check_cuda("out", out, q.dtype, 3)
         if out.shape != q.shape:
             raise ValueError(f"out must be {tuple(q.shape)}, got {tuple(out.shape)}")
-    nbytes = int(lib().softmax_attention_decode_workspace_size(N, S, P, H, Hk, D, dt))
-    ws = _workspace(nbytes, q.device, workspace) if nbytes or workspace is not None else None
-    st = lib().softmax_attention_decode_step(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
-                                             _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None,
-                                             _scale(scale), _ptr(out), N, S, P, H, Hk, D, dt, _ptr(device_status),
-                                             _ptr(ws), 0 if ws is None else ws.numel(), _stream())
+    ws = workspace
+    if ws is not None:
+        _check("workspace", ws, torch.uint8)
+    while True:
+        st = lib().softmax_attention_decode_step(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(lengths),
+                                                 _ptr(prefix_k) if P else None, _ptr(prefix_v) if P else None,
+                                                 _scale(scale), _ptr(out), N, S, P, H, Hk, D, dt, _ptr(device_status),
+                                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream())
+        if st != SGLA_ERR_WORKSPACE or ws is not None:
+            break
+        # there are parts to join (nothing was launched): only then is a workspace needed
+        nbytes = int(lib().softmax_attention_decode_workspace_size(N, S, P, H, Hk, D, dt))
+        ws = _workspace(nbytes, q.device, None)
+    if st == SGLA_ERR_WORKSPACE:
+        raise ValueError("workspace is smaller than softmax_attention_decode_workspace_size")
     raise_for_status(st, "softmax_attention_decode_step")
     return out
 
 
 def _rotary(q, k, positions, inv_freq, axes, interleaved, inverse, where):
     dt = _operands((("q", q),) if k is None else (("q", q), ("k", k)))
-    if q.dim() < 2:
+    shape = q.shape
+    if len(shape) < 2:
         raise ValueError("q must be [..., H, D]")
-    lead, (H, D) = q.shape[:-2], q.shape[-2:]
+    lead, H, D = shape[:-2], shape[-2], shape[-1]
     Hk = 0
     if k is not None:
-        if k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != D:
-            raise ValueError(f"k must be [..., Hk, D] with q's leading and last dimensions, got {tuple(k.shape)}")
-        Hk = k.shape[-2]
-    _check_cuda("positions", positions, torch.int64)
-    if positions.shape == lead:
+        kshape = k.shape
+        Hk = kshape[-2] if len(kshape) > 1 else 0
+        if kshape != (*lead, Hk, D):
+            raise ValueError(f"k must be [..., Hk, D] with q's leading and last dimensions, got {tuple(kshape)}")
+    _check("positions", positions, torch.int64)
+    pshape = positions.shape
+    if pshape == lead:
         A = 1
-    elif positions.shape[:-1] == lead and positions.shape[-1] >= 1:
-        A = positions.shape[-1]
+    elif len(pshape) == len(lead) + 1 and pshape[:-1] == lead and pshape[-1] >= 1:
+        A = pshape[-1]
     else:
-        raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead)} + (axes,), got {tuple(positions.shape)}")
-    _check_cuda("inv_freq", inv_freq, torch.float32, 1)
+        raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead)} + (axes,), got {tuple(pshape)}")
+    _check("inv_freq", inv_freq, torch.float32, 1)
     half = inv_freq.shape[0]
     if 2 * half > D:
         raise ValueError(f"inv_freq has {half} pairs, a head of {D} has {D // 2}")
     table = bytes(half) if axes is None else bytes(axes)
-    if len(table) != half or (half and max(table) >= A):
-        raise ValueError(f"axes must hold one axis below {A} for each of the {half} pairs")
+    if len(table) != half or A > 255:  # an axis that is not below A is refused by the library
+        raise ValueError(f"axes must hold one axis below {A} for each of the {half} pairs, {A} at most 255")
     qo = torch.empty_like(q)
     ko = None if k is None else torch.empty_like(k)
-    st = lib().multi_axis_rotary(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), table, _ptr(qo), _ptr(ko),
-                                 lead.numel(), H, Hk, D, 2 * half, A, int(bool(interleaved)), int(inverse), dt,
-                                 _stream())
+    st = lib().multi_axis_rotary(q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(), table, qo.data_ptr(),
+                                 _ptr(ko), lead.numel(), H, Hk, D, 2 * half, A, 1 if interleaved else 0,
+                                 1 if inverse else 0, dt, _stream())
     raise_for_status(st, where)
     return qo, ko
 
