@@ -328,7 +328,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         bool ok = true;
         while (ok && feed.take(ni, it)) {
             const bool mine = tr < R && x < it.q_left;
-            const int n = it.nt[w];
+            const int n = w == 0 ? it.nt[0] : it.nt[1];
             const int lim = mine ? (a.causal ? min(it.keys, x + 1 + it.shift) : it.keys) : 0;  // keys the row sees
             float m = -INFINITY, l = 0.f;  // m in units of S
             for (int j = 0; j < n; ++j, ++ns) {

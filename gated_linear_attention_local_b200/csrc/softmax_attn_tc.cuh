@@ -7,9 +7,9 @@
 namespace sgla {
 namespace {
 
-// Registers a thread of a 384-thread kernel: 168 at launch; its eight row warps take 208, the
-// others keep 80 (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
-constexpr int kRowRegs = 208, kOtherRegs = 80;
+// Registers a thread of a 384-thread kernel: 168 at launch; its eight row warps take 224, the
+// others keep 48 (256 * 224 + 128 * 48 = 63488 of 384 * 168 = 64512).
+constexpr int kRowRegs = 224, kOtherRegs = 48;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Exponentials on the FMA pipe: with n = round(x), f = x - n, 2^x = 2^n p3(f), p3 the degree-3
