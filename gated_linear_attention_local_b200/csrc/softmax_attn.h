@@ -127,7 +127,8 @@ __device__ __forceinline__ bool attn_locate(const AttnArgs &a, bool own_q, int64
     int64_t first = 0;  // first slot of the sequence
     if (own.cu && a.status && slot < a.N && (threadIdx.x & 31) == 0) {  // every sequence is checked once, found or not
         int64_t s0, n0;
-        if (!attn_span(a.sq, a.N, slot, s0, n0) || !attn_span(a.sk, a.N, slot, s0, n0))
+        if (!attn_span(a.sq, a.N, slot, s0, n0) || !attn_span(a.sk, a.N, slot, s0, n0) ||
+            (slot == 0 && (a.sq.cu[0] != 0 || a.sk.cu[0] != 0)))
             atomicExch(a.status, kDevBadCuSeqlens);
     }
     if (!own.cu) {

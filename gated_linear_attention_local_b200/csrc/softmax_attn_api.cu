@@ -12,7 +12,8 @@ namespace {
 
 using namespace sgla;
 
-constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+// every token index and difference of two, doubled, fits 32 bits in the kernels
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -233,6 +234,7 @@ sgla_status softmax_attention_decode_step(const void *q, const void *k_cache, co
         a.split = p.psplit; a.nsplit = p.pparts;
         a.part_o = part_o;
         a.part_lse = part_lse;
+        a.status = device_status;
         ATTN_LAUNCH("softmax_attention_prefix", launch_fwd(a, st));
     }
     a.k = k_cache; a.v = v_cache;

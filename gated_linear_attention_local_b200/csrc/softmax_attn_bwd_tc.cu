@@ -350,7 +350,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
         const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
         const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
-        auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+        auto wait = [&](uint64_t *bar, uint32_t ph) { return all_wait(bar, ph, abort_flag); };
         KvItem it;
         int ni = 0;
         uint32_t own_ph = 0, ph = 0;  // parity of the item's own tiles; of p and ds of the tile in turn
@@ -605,6 +605,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
         const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
         const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
         const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
+        // (the lanes poll as one; all_wait's vote here: 177 -> 180 us at 2 x 4096 tokens of 16 heads)
         auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
         QItem it;
         int ni = 0;

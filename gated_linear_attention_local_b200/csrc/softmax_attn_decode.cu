@@ -349,8 +349,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant
     int done = 0;
     for (; done < mine; ++done) {
         const int st = done % C::STAGES;
-        if (!mbar_wait(&full[st], (done / C::STAGES) & 1, abort_flag)) break;
-        __syncwarp();
+        // (one answer for all lanes: none is left behind at a warp-wide instruction)
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (done / C::STAGES) & 1, abort_flag))) break;
         unsigned char *kt = ring + st * C::STAGE, *vt = kt + C::TILE;
         const int valid = (int)min64(kKeys, len - (beg + warp + (int64_t)done * kWarps) * kKeys);
         if (valid < kKeys) {

@@ -55,6 +55,12 @@ __device__ __forceinline__ void store_cols32(__nv_bfloat16 *dst, const float (&o
 }
 inline bool wide_rows(const void *p, int D) { return D % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
 
+// mbar_wait by all lanes of a warp, with one answer for all: a lane that gave up must not leave the
+// others at a warp-wide instruction.
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
 // Work items of a kernel whose grid has a block for every item but whose CTAs stay on their SM: a
 // scheduler warp takes over blocks that have not started (clusterlaunchcontrol), describes them
 // and hands the description to the other warps.  It asks when the copies of the item in work
@@ -77,7 +83,7 @@ struct Feed {
     }
     // The next item, by all lanes of a warp; false when there is none.
     __device__ bool take(int &count, Item &it) const {
-        if (!mbar_wait(full, count & 1, abort_flag)) return false;
+        if (!all_wait(full, count & 1, abort_flag)) return false;
         it = *item;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
@@ -91,8 +97,7 @@ struct Feed {
         int count = 0;
         bool ok = true;
         auto publish = [&](const Item &it) {
-            if (count > 0) ok = mbar_wait_idle(empty, (count - 1) & 1, abort_flag);
-            __syncwarp();
+            if (count > 0) ok = __all_sync(0xffffffffu, mbar_wait_idle(empty, (count - 1) & 1, abort_flag));
             if (ok && lane == 0) {
                 *item = it;
                 mbar_arrive(full);
@@ -104,7 +109,7 @@ struct Feed {
             Item it;
             if (describe(u, it)) {
                 publish(it);
-                if (!ok || !(ok = mbar_wait_idle(want, (count - 1) & 1, abort_flag))) break;
+                if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait_idle(want, (count - 1) & 1, abort_flag)))) break;
             }
             __syncwarp();
             if (lane == 0) {
@@ -113,7 +118,10 @@ struct Feed {
                 next_block_request(answer, next);
             }
             __syncwarp();
-            if (!(ok = mbar_wait(next, asked & 1, abort_flag))) break;
+            if (!(ok = all_wait(next, asked & 1, abort_flag))) {
+                if (lane == 0) mbar_drain(next, asked & 1);  // no answer into shared memory that is given up
+                break;
+            }
             ++asked;
             u = next_block_answer(answer);
             __syncwarp();

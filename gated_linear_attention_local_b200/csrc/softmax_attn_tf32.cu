@@ -576,6 +576,7 @@ cudaError_t launch_part(int part, const AttnArgs &a, cudaStream_t st) {
     const size_t tile = (size_t)kB * Stride<DP>::value;
     const int64_t nq = attn_slots(a.sq, a.N, a.G, kB), nk = attn_slots(a.sk, a.N, 1, kB);
     const int64_t rows = (a.sq.cu ? a.sq.T / a.N : a.sq.T) * a.G, keys = a.sk.cu ? a.sk.T / a.N : a.sk.T;
+    if (std::max(nq, nk) >= (int64_t)1 << 28) return cudaErrorInvalidValue;  // times 8 CTAs: past the grid's limit
     const dim3 gq((unsigned)nq, a.Hk, part == 0 ? a.nsplit : 1), gk((unsigned)nk, a.Hk);
     if (part == 0)
         return launch(attn_fwd_tf32_kernel<DP>, gq, cluster_size(nq * a.Hk * a.nsplit, std::min(keys, a.split)),

@@ -512,16 +512,19 @@ SGLA_API sgla_status simple_gla_normalized_decode_step(const void *q, const void
  *   cu_seqlens_q == cu_seqlens_k == NULL: N sequences of Tq queries and Tk keys.
  *   Both given: DEVICE pointers to N+1 int64 (N >= 1; they may be one array), Tq and Tk
  *       the token counts in all.  A sequence whose bounds are not 0 <= start <= end <= T
- *       on both sides is skipped (its outputs are not written) and *device_status, when
- *       given, is set to SGLA_DEVICE_BAD_CU_SEQLENS.  Tokens behind the last sequence
- *       belong to none: their outputs are zeros (lse -inf).
- *   device_status: optional DEVICE int, reset to SGLA_DEVICE_OK by these calls.
+ *       on both sides is skipped (its outputs are not written), so are tokens in front of
+ *       the first sequence; *device_status, when given, is then set to
+ *       SGLA_DEVICE_BAD_CU_SEQLENS.  Tokens behind the last sequence belong to none: their
+ *       outputs are zeros (lse -inf).
+ *   device_status: optional DEVICE int, reset to SGLA_DEVICE_OK by these calls;
+ *       SGLA_DEVICE_TIMEOUT when a wait of a tensor-core pipeline gave up (as the workspace
+ *       status of the other calls).
  *   scale as simple_gla_fwd (NaN or <= 0 selects 1/sqrt(D)).
  * Only what a query sees is meant to be finite for its output to be; a value that is not
  * finite in a key or value later in the same tile of 128 keys can reach a causal query as
  * NaN (0 times it).  Keys behind a sequence's end are never read into a result.
  * Supported sizes: D <= 128 and a multiple of 8, H a multiple of Hk, H / Hk <= 128,
- * H <= 65535, fewer than 2^31 tokens.  Tensor pointers 16-byte aligned.
+ * H <= 65535, fewer than 2^30 tokens.  Tensor pointers 16-byte aligned.
  * Results do not depend on the order in which thread blocks run (no atomics).
  *
  * softmax_attention_bwd: dq, dk, dv for the loss sum(o dout), with o and lse those of
@@ -549,7 +552,7 @@ SGLA_API sgla_status softmax_attention_bwd(const void *q, const void *k, const v
  *   key among them, if it is to be seen).  What lies behind lengths[n] is not read into
  *   the result.  A length outside that range counts as 0 and sets *device_status (optional
  *   DEVICE int, reset by the call) to SGLA_DEVICE_BAD_CU_SEQLENS.  No key at all: o = 0.
- * Heads, D, scale, alignment as softmax_attention_fwd; N * max(S, H) < 2^31.  workspace:
+ * Heads, D, scale, alignment as softmax_attention_fwd; P and N * max(S, H) below 2^30.  workspace:
  * softmax_attention_decode_workspace_size() bytes (0: none needed), 256-byte aligned.
  */
 SGLA_API size_t softmax_attention_decode_workspace_size(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk,

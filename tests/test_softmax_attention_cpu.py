@@ -31,7 +31,8 @@ def test_forward_refusals(lib):
     assert fwd(lib, cu=P) == INV and fwd(lib, cuk=P) == INV and fwd(lib, cu=P, cuk=P, N=0) == INV
     assert fwd(lib, cu=P + 4, cuk=P) == INV and fwd(lib, dt=7) == INV
     assert fwd(lib, D=136) == UNS and fwd(lib, D=12) == UNS and fwd(lib, H=258, Hk=2) == UNS
-    assert fwd(lib, H=65536, Hk=65536) == UNS and fwd(lib, N=1 << 20, Tq=1 << 11) == UNS
+    assert fwd(lib, H=65536, Hk=65536) == UNS and fwd(lib, N=1 << 20, Tq=1 << 10) == UNS
+    assert fwd(lib, cu=P, cuk=P, Tk=1 << 30) == UNS
     assert fwd(lib, N=0) == 0 and fwd(lib, Tq=0, q=None, o=None) == 0  # nothing to do
 
 
@@ -55,7 +56,7 @@ def test_decode_refusals(lib):
     assert dec(q=None) == INV and dec(kc=None) == INV and dec(ln=None) == INV and dec(o=None) == INV
     assert dec(Pn=3) == INV and dec(Pn=3, pk=P) == INV and dec(Pn=-1) == INV and dec(ln=P + 4) == INV
     assert dec(vc=P + 8) == INV and dec(H=3) == INV and dec(D=129) == UNS and dec(D=136) == UNS
-    assert dec(N=1 << 20, S=1 << 11) == UNS
+    assert dec(N=1 << 20, S=1 << 10) == UNS and dec(Pn=1 << 30, pk=P, pv=P) == UNS
     for kw in (dict(Pn=500, pk=P, pv=P), dict(H=64, Hk=2)):  # parts to join: a prefix, a large group
         assert dec(ws=None, **kw) == WS and dec(n=100, **kw) == WS and dec(ws=P + 16, **kw) == INV
     assert dec(N=0) == 0
@@ -152,6 +153,7 @@ def test_binding_refusals(refuses):
     refuses(ValueError, d, qt, k, k, ln, out=fake(2, 4, 32))
     pos, fr = fake(2, 8, 3, dtype=i64), fake(32, dtype=torch.float32)
     refuses(ValueError, r, q, k, pos, fr, axes=[0] * 31)
+    refuses(TypeError, r, q, k, pos, fr, axes=32)
     refuses(ValueError, r, q, k, pos, fr, axes=[0] * 31 + [3])
     refuses(ValueError, r, q, k, pos, fr, axes=[0] * 31 + [-1])
     refuses(ValueError, r, q, k, fake(2, 7, 3, dtype=i64), fr)

@@ -115,7 +115,7 @@ def test_neighbours_do_not_leak(dtype):
 def test_bad_cu_seqlens_is_reported():
     q = torch.randn(100, 2, 64, device="cuda", dtype=BF16)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    for cu in ([0, 60, 50, 100], [0, 50, 101], [-1, 50, 100], [0, 1 << 40, 100]):
+    for cu in ([0, 60, 50, 100], [0, 50, 101], [-1, 50, 100], [0, 1 << 40, 100], [1, 50, 100]):
         o, lse = sg.softmax_attention_fwd(q, q, q, cu_seqlens=torch.tensor(cu).cuda(), device_status=status)
         assert int(status) == 1, cu
     good = torch.tensor([0, 50, 100]).cuda()
@@ -230,6 +230,13 @@ def test_decode_step(case, dtype):
     ref.check(o, decode_reference(q, kc, vc, lengths, pk, pv), "o")
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("G,P", [(15, 0), (16, 0), (16, 140), (17, 0), (17, 140)])
+def test_decode_group_sizes(G, P, dtype):
+    """On both sides of the largest group that the streaming kernel takes."""
+    test_decode_step((3, 520, [1, 519, 260], P, 2 * G, 2, 64), dtype)
+
+
 def test_decode_bad_length_counts_as_empty():
     q = torch.randn(3, 2, 64, device="cuda", dtype=BF16)
     kc = torch.randn(3, 50, 2, 64, device="cuda", dtype=BF16)
@@ -271,6 +278,52 @@ def test_decode_cache_past_32_bit_offsets():
     o = sg.softmax_attention_decode_step(q, kc, vc, torch.tensor([1, 1, S]).cuda())
     want = ref.attention(q[2:, None, 1000:], kc[2:, :, 1000:], vc[2:, :, 1000:], False)["o"]
     ref.check(o[2, 1000:], tuple(x[0, 0] for x in want), "o")
+
+
+def test_packed_tokens_past_32_bit_offsets():
+    """The last sequence of a pack lies more than 2^31 elements into q, o, do and dq."""
+    T, H, D = 132000, 128, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    cu = torch.tensor([*range(0, T - 500, 500), T - 150, T], dtype=torch.int64).cuda()
+    gen = torch.Generator().manual_seed(21)
+    q, do = (torch.zeros(T, H, D, device="cuda", dtype=BF16) for _ in range(2))
+    k, v = (normal(gen, T, 1, D, dtype=BF16) for _ in range(2))
+    last = slice(T - 150, T)
+    q[last], do[last] = normal(gen, 150, H, D, dtype=BF16), normal(gen, 150, H, D, dtype=BF16)
+    o, lse = sg.softmax_attention_fwd(q, k, v, cu_seqlens=cu)
+    r = sg.softmax_attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu)
+    want = ref.attention(q[None, last], k[None, last], v[None, last], True, do=do[None, last])
+    for name, got in (("o", o), ("lse", lse), *r.items()):
+        ref.check(got[None, last], want[name], name)
+
+
+def test_two_streams_at_once():
+    """Calls that run at the same time share nothing: each stream's results as alone."""
+    gen = torch.Generator().manual_seed(22)
+    sets = [[normal(gen, 2, 700, 8, 64, dtype=BF16)] + [normal(gen, 2, 700, 2, 64, dtype=BF16) for _ in range(2)]
+            for _ in range(2)]
+    kc = normal(gen, 4, 900, 2, 64, dtype=BF16)
+    ln = torch.tensor([900, 1, 450, 0]).cuda()
+
+    def work(q, k, v):
+        o, lse = sg.softmax_attention_fwd(q, k, v)
+        r = sg.softmax_attention_bwd(q, k, v, o, lse, q)
+        step = sg.softmax_attention_decode_step(q[0, :4].contiguous(), kc, kc, ln, k[0], v[0])
+        return [o, lse, r["dq"], r["dk"], r["dv"], step]
+
+    want = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(10):
+        for st, s, out in zip(streams, sets, got):
+            with torch.cuda.stream(st):
+                out.append(work(*s))
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        for x in out:
+            assert all(torch.equal(a, b) for a, b in zip(x, w))
 
 
 def test_captured_and_replayed():
