@@ -167,6 +167,73 @@ __device__ __forceinline__ bool attn_locate(const AttnArgs &a, bool own_q, int64
     return t.row0 >= 0 && t.row0 < (own_q ? t.tq : t.tk) * mul;
 }
 
+// The row tiles of a packed batch of up to kMax - 1 sequences, last ones (which see the most keys)
+// first and over all sequences at once, so that no long tile is left for the end: the u-th tile is
+// found from the sequences' tile counts, which one warp keeps in registers.  Against sequence by
+// sequence: forward of 8 sequences, 16868 tokens in all, 185 -> 178 us.  (The backward kernels
+// gained nothing: their items are half as long.)
+struct AttnOrder {
+    static constexpr int kPer = 8, kMax = 32 * kPer;
+    bool on = false;
+    int tiles[kPer];  // of sequences lane + 32 i; sequence N: the tokens behind the last
+
+    // By all lanes of a warp; tiles of `div` tokens.
+    __device__ __forceinline__ void init(const AttnArgs &a, int div) {
+        on = a.sq.cu && a.N < kMax;
+        if (!on) return;
+        const int lane = threadIdx.x & 31;
+        bool bad = a.sq.cu[0] != 0 || a.sk.cu[0] != 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int n = lane + 32 * i;
+            tiles[i] = 0;
+            int64_t q0, tq, k0, tk;
+            if (n > a.N) continue;
+            if (attn_span(a.sq, a.N, n, q0, tq) && attn_span(a.sk, a.N, n, k0, tk))
+                tiles[i] = (int)((tq + div - 1) / div);
+            else
+                bad = true;
+        }
+        if (bad && a.status) atomicExch(a.status, kDevBadCuSeqlens);
+        __syncwarp();
+    }
+    __device__ __forceinline__ int above(int level) const {  // tiles whose index in their sequence is at least level
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) c += max(tiles[i] - level, 0);
+        return __reduce_add_sync(0xffffffffu, c);
+    }
+    // Tile u in that order; false when there are no more.
+    __device__ __forceinline__ bool locate(const AttnArgs &a, int u, int div, AttnTile &t) const {
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) most = max(most, tiles[i]);
+        int lo = 0, hi = __reduce_max_sync(0xffffffffu, most);
+        if (u >= above(0)) return false;
+        while (hi - lo > 1) {  // above(lo) > u >= above(hi)
+            const int mid = lo + (hi - lo) / 2;
+            if (above(mid) > u) lo = mid;
+            else hi = mid;
+        }
+        int rank = u - above(lo + 1);  // among the sequences that have a tile `lo`
+        t.n = -1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int lane = threadIdx.x & 31;
+            const unsigned m = __ballot_sync(0xffffffffu, tiles[i] > lo);
+            const unsigned pick = __ballot_sync(0xffffffffu, tiles[i] > lo && __popc(m & ((1u << lane) - 1)) == rank);
+            if (t.n < 0 && pick) t.n = 32 * i + __ffs(pick) - 1;
+            rank -= __popc(m);
+        }
+        if (t.n < 0) return false;
+        attn_span(a.sq, a.N, t.n, t.q0, t.tq);
+        attn_span(a.sk, a.N, t.n, t.k0, t.tk);
+        if (t.n == a.N) t.tk = 0;  // behind the last sequence: zeros
+        t.row0 = (int64_t)lo * div;
+        return t.row0 < t.tq;
+    }
+};
+
 __host__ __device__ __forceinline__ int64_t attn_slots(const AttnSeqs &s, int64_t N, int mul, int div) {
     return s.cu ? s.T * mul / div + N + 1 : N * ((s.T * mul + div - 1) / div);
 }

@@ -102,7 +102,7 @@ __device__ __forceinline__ void probabilities(const float (&s)[32], float sc, fl
     tmem_st16(taddr, p);
 }
 
-template <int DP>
+template <int DP, bool PACKED>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, AttnArgs a, int R, int slots,
@@ -150,15 +150,21 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // ---------------------------------------------------------------- scheduler
         setmaxnreg_dec<kOtherRegs>();
         const int per_z = slots * a.Hk;
+        AttnOrder order;
+        if constexpr (PACKED) order.init(a, 2 * R);
         feed.run([&](int u, Item &it) -> bool {
             it.z = u / per_z;
             const int rest = u - it.z * per_z;
             it.hk = rest % a.Hk;
-            // heaviest first: a causal sequence's last rows see the most keys
-            int64_t slot = slots - 1 - rest / a.Hk;
-            if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
             AttnTile t;
-            if (!attn_locate(a, true, slot, 1, 2 * R, t)) return false;
+            if (PACKED && order.on) {
+                if (!order.locate(a, rest / a.Hk, 2 * R, t)) return false;
+            } else {
+                // heaviest first: a causal sequence's last rows see the most keys
+                int64_t slot = slots - 1 - rest / a.Hk;
+                if (!PACKED) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+                if (!attn_locate(a, true, slot, 1, 2 * R, t)) return false;
+            }
             const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
             it.keys = (int)(ke > kb ? ke - kb : 0);
             it.q_tok = (int)(t.q0 + t.row0);
@@ -446,10 +452,10 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
 }
 
-template <int DP>
+template <int DP, bool PACKED>
 cudaError_t launch_fwd(const AttnArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int R,
                        cudaStream_t st) {
-    auto kern = attn_fwd_tc_kernel<DP>;
+    auto kern = attn_fwd_tc_kernel<DP, PACKED>;
     constexpr size_t smem = FwdCfg<DP>::SMEM;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, smem, done);
@@ -474,7 +480,9 @@ cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t st) {
     } else {
         tk = tv = tq;  // no key anywhere: never used
     }
-    return a.D <= 64 ? launch_fwd<64>(a, tq, tk, tv, R, st) : launch_fwd<128>(a, tq, tk, tv, R, st);
+    if (a.sq.cu)
+        return a.D <= 64 ? launch_fwd<64, true>(a, tq, tk, tv, R, st) : launch_fwd<128, true>(a, tq, tk, tv, R, st);
+    return a.D <= 64 ? launch_fwd<64, false>(a, tq, tk, tv, R, st) : launch_fwd<128, false>(a, tq, tk, tv, R, st);
 }
 
 }  // namespace sgla

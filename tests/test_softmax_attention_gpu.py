@@ -64,6 +64,9 @@ PACKED = [
     ([3, 130], [0, 257], 0, 3, 3, 128, False),
     ([1] * 70 + [250], None, 9, 2, 1, 64, True),
     ([9] * 1100, None, 0, 1, 1, 32, True),
+    ([3] * 200 + [140] + [2] * 54, None, 5, 2, 2, 64, True),
+    ([3] * 200 + [140] + [2] * 55, None, 5, 2, 2, 64, True),
+    ([1, 700, 40, 390], [800, 1, 0, 400], 11, 4, 1, 96, False),
 ]
 
 
