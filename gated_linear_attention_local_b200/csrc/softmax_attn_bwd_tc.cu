@@ -27,8 +27,13 @@
 // exponentials runs on the FMA pipe (see softmax_attn_tc.cuh).
 //
 // The CTAs stay on their SM and take item after item (Feed, softmax_attn_tc.cuh; against a CTA
-// an item: packed training MEASURED): the copies and first products of an item run under
-// the stores of the one before.
+// an item: the three kernels of packed training 500 -> 427 us when it came): the copies and first
+// products of an item run under the stores of the one before.
+//
+// Measured: 2 x 4096 causal tokens, 16 heads of 128 on 4: dq 176 us, dk dv 221 us (the forward
+// 127); 13 packed sequences of up to 2047 tokens, 12 heads of 64: 135 and 167 us (101).  Bound by
+// the chain of a tile (scores, p, ds, sums) through one buffer of each in tensor memory; heads of
+// 64 besides by products of 64 columns, which take as long as 128.
 //
 // Shared memory (DP = 128): the item's own two tiles 64 KB, rings of three X tiles (Q or K, read
 // by the first and the last product of a tile) and two Y tiles (dO or V), 160 KB.
