@@ -10,7 +10,7 @@ models").  Argument marshalling for the entry points of ``include/simple_gla.h``
 """
 from __future__ import annotations
 
-import ctypes
+import math
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -216,21 +216,19 @@ def softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, p
 
 def _rotary(q, k, positions, inv_freq, axes, interleaved, inverse, where):
     dt = _operands((("q", q),) if k is None else (("q", q), ("k", k)))
-    shape = q.shape
-    if len(shape) < 2:
+    if q.dim() < 2:
         raise ValueError("q must be [..., H, D]")
-    lead, H, D = shape[:-2], shape[-2], shape[-1]
+    *lead, H, D = q.shape
     Hk = 0
     if k is not None:
-        kshape = k.shape
-        Hk = kshape[-2] if len(kshape) > 1 else 0
-        if kshape != (*lead, Hk, D):
-            raise ValueError(f"k must be [..., Hk, D] with q's leading and last dimensions, got {tuple(kshape)}")
+        *klead, Hk, Dk = k.shape if k.dim() > 1 else (0, 0)
+        if klead != lead or Dk != D:
+            raise ValueError(f"k must be [..., Hk, D] with q's leading and last dimensions, got {tuple(k.shape)}")
     _check("positions", positions, torch.int64)
-    pshape = positions.shape
+    pshape = [*positions.shape]
     if pshape == lead:
         A = 1
-    elif len(pshape) == len(lead) + 1 and pshape[:-1] == lead and pshape[-1] >= 1:
+    elif pshape and pshape[:-1] == lead and pshape[-1] >= 1:
         A = pshape[-1]
     else:
         raise ValueError(f"positions must be {tuple(lead)} or {tuple(lead)} + (axes,), got {tuple(pshape)}")
@@ -246,7 +244,7 @@ def _rotary(q, k, positions, inv_freq, axes, interleaved, inverse, where):
     qo = torch.empty_like(q)
     ko = None if k is None else torch.empty_like(k)
     st = lib().multi_axis_rotary(q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(), table, qo.data_ptr(),
-                                 _ptr(ko), lead.numel(), H, Hk, D, 2 * half, A, 1 if interleaved else 0,
+                                 _ptr(ko), math.prod(lead), H, Hk, D, 2 * half, A, 1 if interleaved else 0,
                                  1 if inverse else 0, dt, _stream())
     raise_for_status(st, where)
     return qo, ko
