@@ -44,8 +44,8 @@
 #include <algorithm>
 
 #include "softmax_attn.h"
+#include "softmax_attn_map.h"
 #include "softmax_attn_tc.cuh"
-#include "tc_path.h"
 
 namespace sgla {
 

@@ -28,7 +28,7 @@
 #include <utility>
 
 #include "softmax_attn.h"
-#include "tc_path.h"
+#include "softmax_attn_map.h"
 #include "tc_ptx.cuh"
 #include "tc_tiles.cuh"
 

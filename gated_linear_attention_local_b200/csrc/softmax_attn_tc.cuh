@@ -1,7 +1,7 @@
 // What the tensor-core kernels of softmax attention share.
 #pragma once
 
-#include "tc_ptx.cuh"
+#include "softmax_attn_ptx.cuh"
 #include "tc_tiles.cuh"
 
 namespace sgla {

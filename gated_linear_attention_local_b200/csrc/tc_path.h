@@ -39,11 +39,6 @@ cudaError_t tc_launch_segment_state(const FwdArgs &a, cudaStream_t st);
 // 3-D TMA map over a [tokens, H, D] bf16 tensor, box [128 tokens x 1 head x box],
 // box = 64 (128-byte swizzle) or 32 (64-byte swizzle).
 cudaError_t tc_make_map(CUtensorMap *m, const void *ptr, int64_t tokens, int H, int D, int box);
-// 3-D TMA map over a [tokens, H, D] tensor, box [box_tokens x box_heads x 128 bytes of
-// columns] (64 bf16 or 32 fp32), 128-byte swizzle: the rows (token, head) of a box land as
-// consecutive 128-byte rows.
-cudaError_t tc_make_map_rows(CUtensorMap *m, const void *ptr, int64_t tokens, int H, int D, int box_heads,
-                             int box_tokens, bool f32 = false);
 cudaError_t tc_launch_chunk_output(const FwdArgs &a, cudaStream_t st);
 // The K = 128 walk (walk_k128.cu): V tiles of 128 columns when V is a multiple of
 // 128, else 64.
