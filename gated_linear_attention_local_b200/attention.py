@@ -85,11 +85,11 @@ def _check_status(device_status):
             raise ValueError("device_status must hold one element")
 
 
-def _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=None):
+def _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=None, want_lse=True):
     N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
     _check_status(device_status)
     o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
     st = lib().softmax_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _scale(scale), int(bool(causal)), _ptr(o), _ptr(lse),
                                      _ptr(cu_seqlens), _ptr(cu_k), N, Tq, Tk, H, Hk, D, dt, _ptr(device_status),
                                      _stream())
@@ -156,7 +156,7 @@ def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seql
     gradients are enabled and one of them requires gradients."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
-    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)[0]
+    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, want_lse=False)[0]
 
 
 @_on_tensor_device

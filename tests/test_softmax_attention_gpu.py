@@ -424,3 +424,14 @@ def test_profile_records_the_kernels():
     assert _lib.kernel_launch_count() == n + sum(c for c, _ in rec.values())
     assert set(rec) == {"softmax_attention_fwd", "softmax_attention_delta", "softmax_attention_dkdv",
                         "softmax_attention_dq"}
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_output_alone_is_the_forwards(dtype):
+    """softmax_attention without gradients (no lse is formed) gives softmax_attention_fwd's output."""
+    gen = torch.Generator().manual_seed(23)
+    q, k, v = (normal(gen, 2, 200, 2, 64, dtype=dtype) for _ in range(3))
+    want, _ = sg.softmax_attention_fwd(q, k, v)
+    assert torch.equal(sg.softmax_attention(q, k, v), want)
+    with torch.no_grad():
+        assert torch.equal(sg.softmax_attention(q.clone().requires_grad_(), k, v), want)
