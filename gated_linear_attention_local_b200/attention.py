@@ -47,35 +47,35 @@ def _operands(named):
 def _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k):
     """Checks of the forward and backward; returns (N, Tq, Tk, H, Hk, D, dtype, cu_k)."""
     dt = _operands((("q", q), ("k", k), ("v", v)))
+    qs, ks = q.shape, k.shape
     if cu_seqlens is None:
         if cu_seqlens_k is not None:
             raise ValueError("cu_seqlens_k needs cu_seqlens")
-        if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+        if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0]:
             raise ValueError("q must be [B,T,H,D] and k, v [B,S,Hk,D]")
-        N = q.shape[0]
+        N = qs[0]
     else:
         _check("cu_seqlens", cu_seqlens, torch.int64, 1)
         _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int64, 1)
-        if q.dim() not in (3, 4) or k.dim() != q.dim():
+        if len(qs) not in (3, 4) or len(ks) != len(qs):
             raise ValueError("with cu_seqlens q must be [T,H,D] or [1,T,H,D], and k, v alike")
-        if q.dim() == 4 and (q.shape[0] != 1 or k.shape[0] != 1):
+        if len(qs) == 4 and (qs[0] != 1 or ks[0] != 1):
             raise ValueError("with cu_seqlens the batch size must be 1 (flatten the batch first)")
         N = cu_seqlens.shape[0] - 1
         if N < 1:
             raise ValueError("cu_seqlens must hold at least two entries")
         if cu_seqlens_k is None:
             cu_seqlens_k = cu_seqlens
-            if k.shape[-3] != q.shape[-3]:
+            if ks[-3] != qs[-3]:
                 raise ValueError("without cu_seqlens_k, k and v must have as many tokens as q")
         elif cu_seqlens_k.shape[0] != N + 1:
             raise ValueError(f"cu_seqlens_k must hold {N + 1} entries like cu_seqlens")
-    if v.shape != k.shape or k.shape[-1] != q.shape[-1]:
+    H, D, Hk = qs[-2], qs[-1], ks[-2]
+    if v.shape != ks or ks[-1] != D:
         raise ValueError("k and v must have one shape, and q, k and v one head dimension")
-    H, D = q.shape[-2:]
-    Hk = k.shape[-2]
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {H} query heads must be a multiple of the {Hk} key heads")
-    return N, q.shape[-3], k.shape[-3], H, Hk, D, dt, cu_seqlens_k
+    return N, qs[-3], ks[-3], H, Hk, D, dt, cu_seqlens_k
 
 
 def _check_status(device_status):
@@ -89,7 +89,7 @@ def _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=Non
     N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
     _check_status(device_status)
     o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if want_lse else None
+    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if want_lse else None
     st = lib().softmax_attention_fwd(_ptr(q), _ptr(k), _ptr(v), _scale(scale), int(bool(causal)), _ptr(o), _ptr(lse),
                                      _ptr(cu_seqlens), _ptr(cu_k), N, Tq, Tk, H, Hk, D, dt, _ptr(device_status),
                                      _stream())
@@ -115,15 +115,15 @@ def softmax_attention_bwd(q, k, v, o, lse, do, causal=True, scale=None, cu_seqle
     N, Tq, Tk, H, Hk, D, dt, cu_k = _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k)
     _check_status(device_status)
     for name, t in (("o", o), ("do", do)):
-        _check_cuda(name, t, q.dtype)
+        _check(name, t, q.dtype)
         if t.shape != q.shape:
             raise ValueError(f"{name} must have the shape of q {tuple(q.shape)}, got {tuple(t.shape)}")
-    _check_cuda("lse", lse, torch.float32)
+    _check("lse", lse, torch.float32)
     if lse.shape != q.shape[:-1]:
         raise ValueError(f"lse must be {tuple(q.shape[:-1])}, got {tuple(lse.shape)}")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    nbytes = int(lib().softmax_attention_bwd_workspace_size(q.shape[:-2].numel(), H))
-    ws = _workspace(nbytes, q.device, workspace)
+    nbytes = max(256, lib().softmax_attention_bwd_workspace_size(q.numel() // (H * D) if H * D else 0, H))
+    ws = q.new_empty(nbytes, dtype=torch.uint8) if workspace is None else _workspace(nbytes, q.device, workspace)
     st = lib().softmax_attention_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _scale(scale),
                                      int(bool(causal)), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(cu_seqlens), _ptr(cu_k), N,
                                      Tq, Tk, H, Hk, D, dt, _ptr(device_status), _ptr(ws), ws.numel(), _stream())
