@@ -305,128 +305,129 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 10) {
-        // ---------------------------------------------------------------- scheduler
+    // (one instruction a warpgroup, ahead of the roles: setmaxnreg is .aligned)
+    if (warp >= 8) {
         setmaxnreg_dec<kOtherRegs>();
-        feed.run([&](int u, KvItem &it) -> bool {
-            it.hk = u % a.Hk;
-            int64_t slot = u / a.Hk;
-            // the first keys are seen by the most rows: every sequence's first tiles first
-            if (!a.sk.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
-            AttnTile t;
-            if (!attn_locate(a, false, slot, 1, kTile, t)) return false;
-            const int64_t off = t.tk - t.tq;
-            const int64_t first = a.causal ? max((int64_t)0, t.row0 - off) : 0;  // first token that sees the first key
-            const int64_t b0 = first / R;                                        // its tile
-            it.n = first < t.tq ? (int)((t.tq + R - 1) / R - b0) : 0;
-            it.k_tok = (int)(t.k0 + t.row0);
-            it.k_left = (int)(t.tk - t.row0);
-            it.q_tok = (int)(t.q0 + b0 * R);
-            it.q_left = (int)(t.tq - b0 * R);
-            it.ahead = a.causal ? (int)max(t.row0 - off - b0 * R, -(int64_t)INT_MAX / 2) : -INT_MAX / 2;
-            return true;
-        });
-    } else if (warp == 8) {
-        // ---------------------------------------------------------------- TMA producer
-        setmaxnreg_dec<kOtherRegs>();
-        produce<DP>(
-            sm, b, feed, 2 * C::T, (uint32_t)(C::NG * R * a.G * 128), lane,
-            [&](const KvItem &it, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g) {
-                    tma_load_3d(sm + C::A0 + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok);
-                    tma_load_3d(sm + C::B0 + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok);
-                }
-            },
-            [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(dst + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
-            },
-            [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(dst + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
+        if (warp == 10) {
+            // ---------------------------------------------------------------- scheduler
+            feed.run([&](int u, KvItem &it) -> bool {
+                it.hk = u % a.Hk;
+                int64_t slot = u / a.Hk;
+                // the first keys are seen by the most rows: every sequence's first tiles first
+                if (!a.sk.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+                AttnTile t;
+                if (!attn_locate(a, false, slot, 1, kTile, t)) return false;
+                const int64_t off = t.tk - t.tq;
+                const int64_t first = a.causal ? max((int64_t)0, t.row0 - off) : 0;  // first token that sees the first key
+                const int64_t b0 = first / R;                                        // its tile
+                it.n = first < t.tq ? (int)((t.tq + R - 1) / R - b0) : 0;
+                it.k_tok = (int)(t.k0 + t.row0);
+                it.k_left = (int)(t.tk - t.row0);
+                it.q_tok = (int)(t.q0 + b0 * R);
+                it.q_left = (int)(t.tq - b0 * R);
+                it.ahead = a.causal ? (int)max(t.row0 - off - b0 * R, -(int64_t)INT_MAX / 2) : -INT_MAX / 2;
+                return true;
             });
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- MMA issuer
-        setmaxnreg_dec<kOtherRegs>();
-        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const int nk = (a.D + 15) / 16;
-        const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
-        const uint32_t sbase = smem_u32(sm);
-        const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
-        const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
-        const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
-        auto wait = [&](uint64_t *bar, uint32_t ph) { return all_wait(bar, ph, abort_flag); };
-        KvItem it;
-        int ni = 0;
-        uint32_t own_ph = 0, ph = 0;  // parity of the item's own tiles; of p and ds of the tile in turn
-        Ring<kStX> x1, x0;            // X of the scores' tile, of the sums' tile
-        Ring<kStY> y1, y0;
-        bool ok = true;
-        while (ok && feed.take(ni, it)) {
-            // the same in every lane; the reduction leaves it in a uniform register
-            const int n = __reduce_max_sync(0xffffffffu, it.n);
-            if (n == 0) continue;
-            // rows of tile i that do not exist are zeroed: 0 * NaN must not arise
-            const int whole = it.q_left / R;  // tiles before the first partial one
-            if (!(ok = wait(b.own, own_ph))) break;
-            own_ph ^= 1u;
-            // two blocks of products a tile, each issued without a pause (the pipe holds few
-            // products, so a wait between two blocks is time it idles): dV(i) S(i+1), dK(i) dP(i+1)
-            for (int i = -1; ok && i < n; ++i) {
-                const bool more = i + 1 < n;
-                if (more) {
-                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
-                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
-                }
-                if (i >= 0 && !(ok = wait(b.p, ph))) break;
-                tc_fence_after();
-                if (elect_one()) {
+        } else if (warp == 8) {
+            // ---------------------------------------------------------------- TMA producer
+            produce<DP>(
+                sm, b, feed, 2 * C::T, (uint32_t)(C::NG * R * a.G * 128), lane,
+                [&](const KvItem &it, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g) {
+                        tma_load_3d(sm + C::A0 + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok);
+                        tma_load_3d(sm + C::B0 + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok);
+                    }
+                },
+                [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
+                },
+                [&](const KvItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok + i * R);
+                });
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- MMA issuer
+            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+            const int nk = (a.D + 15) / 16;
+            const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
+            const uint32_t sbase = smem_u32(sm);
+            const uint64_t kd = kdesc(sbase + C::A0), vd = kdesc(sbase + C::B0);
+            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2), ym = sdesc(sbase + C::Y0, kRegion, 1024, 2);
+            auto wait = [&](uint64_t *bar, uint32_t ph) { return all_wait(bar, ph, abort_flag); };
+            KvItem it;
+            int ni = 0;
+            uint32_t own_ph = 0, ph = 0;  // parity of the item's own tiles; of p and ds of the tile in turn
+            Ring<kStX> x1, x0;            // X of the scores' tile, of the sums' tile
+            Ring<kStY> y1, y0;
+            bool ok = true;
+            while (ok && feed.take(ni, it)) {
+                // the same in every lane; the reduction leaves it in a uniform register
+                const int n = __reduce_max_sync(0xffffffffu, it.n);
+                if (n == 0) continue;
+                // rows of tile i that do not exist are zeroed: 0 * NaN must not arise
+                const int whole = it.q_left / R;  // tiles before the first partial one
+                if (!(ok = wait(b.own, own_ph))) break;
+                own_ph ^= 1u;
+                // two blocks of products a tile, each issued without a pause (the pipe holds few
+                // products, so a wait between two blocks is time it idles): dV(i) S(i+1), dK(i) dP(i+1)
+                for (int i = -1; ok && i < n; ++i) {
+                    const bool more = i + 1 < n;
+                    if (more) {
+                        if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                        if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                    }
+                    if (i >= 0 && !(ok = wait(b.p, ph))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (i >= 0) {
+                            issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, y0.s * C::T), idA, i > 0);
+                            mma_commit(&b.empty_y[y0.s]);
+                        }
+                        if (more) {
+                            issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, x1.s * C::T), idS, nk);
+                            mma_commit(b.s);
+                        }
+                    }
+                    __syncwarp();
+                    if (more) {
+                        if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
+                        if (i + 1 >= whole) zero_rows<C::NG>(sm + C::Y0 + y1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                    }
+                    if (i >= 0 && !(ok = wait(&b.ds[0], ph))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (i >= 0) {
+                            issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, x0.s * C::T), idA, i > 0);
+                            mma_commit(&b.empty_x[x0.s]);
+                            if (!more) mma_commit(b.done);
+                        }
+                        if (more) {
+                            issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, y1.s * C::T), idS, nk);
+                            mma_commit(&b.dp[0]);
+                            if (i + 1 == n - 1) mma_commit(b.empty_own);
+                        }
+                    }
+                    __syncwarp();
                     if (i >= 0) {
-                        issue_sum(tmem + C::COL_ACC, tmem + C::COL_S, desc_at(ym, y0.s * C::T), idA, i > 0);
-                        mma_commit(&b.empty_y[y0.s]);
+                        y0.step();
+                        x0.step();
+                        ph ^= 1u;
                     }
                     if (more) {
-                        issue_scores<DP>(tmem + C::COL_S, kd, desc_at(xk, x1.s * C::T), idS, nk);
-                        mma_commit(b.s);
+                        x1.step();
+                        y1.step();
                     }
-                }
-                __syncwarp();
-                if (more) {
-                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
-                    if (i + 1 >= whole) zero_rows<C::NG>(sm + C::Y0 + y1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
-                }
-                if (i >= 0 && !(ok = wait(&b.ds[0], ph))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    if (i >= 0) {
-                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP, desc_at(xm, x0.s * C::T), idA, i > 0);
-                        mma_commit(&b.empty_x[x0.s]);
-                        if (!more) mma_commit(b.done);
-                    }
-                    if (more) {
-                        issue_scores<DP>(tmem + C::COL_DP, vd, desc_at(yk, y1.s * C::T), idS, nk);
-                        mma_commit(&b.dp[0]);
-                        if (i + 1 == n - 1) mma_commit(b.empty_own);
-                    }
-                }
-                __syncwarp();
-                if (i >= 0) {
-                    y0.step();
-                    x0.step();
-                    ph ^= 1u;
-                }
-                if (more) {
-                    x1.step();
-                    y1.step();
                 }
             }
+            __syncwarp();
+            if (elect_one()) {
+                mma_commit(b.drain);
+                mbar_drain(b.drain, 0);
+            }
         }
-        __syncwarp();
-        if (elect_one()) {
-            mma_commit(b.drain);
-            mbar_drain(b.drain, 0);
-        }
-    } else if (warp < 8) {
+    } else {
         // ---------------------------------------------------------------- p, ds and the stores
         setmaxnreg_inc<kRowRegs>();
         const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;  // this warpgroup's columns: rows c0 ..
@@ -504,8 +505,6 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             tc_fence_before();  // the next item's first sums overwrite the accumulators after its P arrives
         }
         if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
-    } else {
-        setmaxnreg_dec<kOtherRegs>();
     }
     __syncwarp();
     tc_fence_before();
@@ -563,111 +562,112 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 10) {
-        // ---------------------------------------------------------------- scheduler
+    // (one instruction a warpgroup, ahead of the roles: setmaxnreg is .aligned)
+    if (warp >= 8) {
         setmaxnreg_dec<kOtherRegs>();
-        feed.run([&](int u, QItem &it) -> bool {
-            it.hk = u % a.Hk;
-            int64_t slot = slots - 1 - u / a.Hk;  // the last rows see the most keys
-            if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
-            AttnTile t;
-            if (!attn_locate(a, true, slot, 1, R, t)) return false;
-            it.q_tok = (int)(t.q0 + t.row0);
-            it.q_left = (int)(t.tq - t.row0);
-            it.k_tok = (int)t.k0;
-            it.keys = (int)t.tk;
-            it.shift = (int)max(min64(t.row0 + t.tk - t.tq, INT_MAX - 256), -(int64_t)INT_MAX / 2);
-            const int seen = a.causal ? min(it.keys, min(R, it.q_left) + it.shift) : it.keys;
-            it.n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
-            return true;
-        });
-    } else if (warp == 8) {
-        // ---------------------------------------------------------------- TMA producer
-        setmaxnreg_dec<kOtherRegs>();
-        produce<DP>(
-            sm, b, feed, 2u * C::NG * R * a.G * 128, C::T, lane,
-            [&](const QItem &it, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g) {
-                    tma_load_3d(sm + C::A0 + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok);
-                    tma_load_3d(sm + C::B0 + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok);
-                }
-            },
-            [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(dst + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok + i * kTile);
-            },
-            [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
-                for (int g = 0; g < C::NG; ++g)
-                    tma_load_3d(dst + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok + i * kTile);
+        if (warp == 10) {
+            // ---------------------------------------------------------------- scheduler
+            feed.run([&](int u, QItem &it) -> bool {
+                it.hk = u % a.Hk;
+                int64_t slot = slots - 1 - u / a.Hk;  // the last rows see the most keys
+                if (!a.sq.cu) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+                AttnTile t;
+                if (!attn_locate(a, true, slot, 1, R, t)) return false;
+                it.q_tok = (int)(t.q0 + t.row0);
+                it.q_left = (int)(t.tq - t.row0);
+                it.k_tok = (int)t.k0;
+                it.keys = (int)t.tk;
+                it.shift = (int)max(min64(t.row0 + t.tk - t.tq, INT_MAX - 256), -(int64_t)INT_MAX / 2);
+                const int seen = a.causal ? min(it.keys, min(R, it.q_left) + it.shift) : it.keys;
+                it.n = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+                return true;
             });
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- MMA issuer
-        setmaxnreg_dec<kOtherRegs>();
-        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const int nk = (a.D + 15) / 16;
-        const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
-        const uint32_t sbase = smem_u32(sm);
-        const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
-        const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
-        const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
-        // (the lanes poll as one; all_wait's vote here: 177 -> 180 us at 2 x 4096 tokens of 16 heads)
-        auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-        QItem it;
-        int ni = 0;
-        uint32_t own_ph = 0;
-        Ring<kStX> x1, x0;  // K of the scores' tile, of the sum's tile
-        Ring<kStY> y1;
-        Ring<2> d1, d0;     // dP's buffers, of the scores' tile, of the sum's tile
-        uint32_t free_ph = 1;  // parity of S's release by the tile before the scores' tile
-        bool ok = true;
-        while (ok && feed.take(ni, it)) {
-            const int n = __reduce_max_sync(0xffffffffu, it.n);
-            if (n == 0) continue;
-            if (!(ok = wait(b.own, own_ph))) break;
-            own_ph ^= 1u;
-            for (int i = -1; ok && i < n; ++i) {
-                if (i + 1 < n) {
-                    if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
-                    const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
-                    if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
-                    if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
-                    if (!(ok = wait(b.sfree, free_ph))) break;  // (the very first passes at once)
-                    free_ph ^= 1u;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
-                        mma_commit(b.s);
-                        issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
-                        mma_commit(&b.dp[d1.s]);
-                        mma_commit(&b.empty_y[y1.s]);
-                        if (i + 1 == n - 1) mma_commit(b.empty_own);
+        } else if (warp == 8) {
+            // ---------------------------------------------------------------- TMA producer
+            produce<DP>(
+                sm, b, feed, 2u * C::NG * R * a.G * 128, C::T, lane,
+                [&](const QItem &it, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g) {
+                        tma_load_3d(sm + C::A0 + g * kRegion, &tq, bar, 64 * g, it.hk * a.G, it.q_tok);
+                        tma_load_3d(sm + C::B0 + g * kRegion, &tdo, bar, 64 * g, it.hk * a.G, it.q_tok);
                     }
-                    __syncwarp();
-                    x1.step();
-                    y1.step();
-                    d1.step();
-                }
-                if (i >= 0) {
-                    if (!(ok = wait(&b.ds[d0.s], d0.ph))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + d0.s * 128, desc_at(xm, x0.s * C::T), idA,
-                                  i > 0);
-                        mma_commit(&b.empty_x[x0.s]);
-                        if (i == n - 1) mma_commit(b.done);
+                },
+                [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tk, bar, 64 * g, it.hk, it.k_tok + i * kTile);
+                },
+                [&](const QItem &it, int i, unsigned char *dst, uint64_t *bar) {
+                    for (int g = 0; g < C::NG; ++g)
+                        tma_load_3d(dst + g * kRegion, &tv, bar, 64 * g, it.hk, it.k_tok + i * kTile);
+                });
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- MMA issuer
+            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+            const int nk = (a.D + 15) / 16;
+            const uint32_t idA = idesc_bf16_f32(128, 16 * nk, false, true);
+            const uint32_t sbase = smem_u32(sm);
+            const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
+            const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
+            const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
+            // (the lanes poll as one; all_wait's vote here: 177 -> 180 us at 2 x 4096 tokens of 16 heads)
+            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+            QItem it;
+            int ni = 0;
+            uint32_t own_ph = 0;
+            Ring<kStX> x1, x0;  // K of the scores' tile, of the sum's tile
+            Ring<kStY> y1;
+            Ring<2> d1, d0;     // dP's buffers, of the scores' tile, of the sum's tile
+            uint32_t free_ph = 1;  // parity of S's release by the tile before the scores' tile
+            bool ok = true;
+            while (ok && feed.take(ni, it)) {
+                const int n = __reduce_max_sync(0xffffffffu, it.n);
+                if (n == 0) continue;
+                if (!(ok = wait(b.own, own_ph))) break;
+                own_ph ^= 1u;
+                for (int i = -1; ok && i < n; ++i) {
+                    if (i + 1 < n) {
+                        if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                        const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
+                        if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
+                        if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
+                        if (!(ok = wait(b.sfree, free_ph))) break;  // (the very first passes at once)
+                        free_ph ^= 1u;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
+                            mma_commit(b.s);
+                            issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
+                            mma_commit(&b.dp[d1.s]);
+                            mma_commit(&b.empty_y[y1.s]);
+                            if (i + 1 == n - 1) mma_commit(b.empty_own);
+                        }
+                        __syncwarp();
+                        x1.step();
+                        y1.step();
+                        d1.step();
                     }
-                    __syncwarp();
-                    x0.step();
-                    d0.step();
+                    if (i >= 0) {
+                        if (!(ok = wait(&b.ds[d0.s], d0.ph))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + d0.s * 128, desc_at(xm, x0.s * C::T), idA,
+                                      i > 0);
+                            mma_commit(&b.empty_x[x0.s]);
+                            if (i == n - 1) mma_commit(b.done);
+                        }
+                        __syncwarp();
+                        x0.step();
+                        d0.step();
+                    }
                 }
             }
+            __syncwarp();
+            if (elect_one()) {
+                mma_commit(b.drain);
+                mbar_drain(b.drain, 0);
+            }
         }
-        __syncwarp();
-        if (elect_one()) {
-            mma_commit(b.drain);
-            mbar_drain(b.drain, 0);
-        }
-    } else if (warp < 8) {
+    } else {
         // ---------------------------------------------------------------- delta, p, ds and the stores
         setmaxnreg_inc<kRowRegs>();
         const int w = warp >> 2, r = threadIdx.x & 127, c0 = w * kHalf;
@@ -775,8 +775,6 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             tc_fence_before();  // the next item's first sum overwrites the accumulator after its dS arrives
         }
         if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
-    } else {
-        setmaxnreg_dec<kOtherRegs>();
     }
     __syncwarp();
     tc_fence_before();

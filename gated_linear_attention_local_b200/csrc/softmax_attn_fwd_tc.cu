@@ -85,6 +85,11 @@ struct FwdCfg {
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
+// The same descriptor, but to the compiler another one for each key tile (0 <= count < 2^30): those
+// of both Q tiles, kept across an item's key tiles, would take 32 of the product warp's 72 registers
+// (8192 tokens of 32 heads: 454 us for 461).
+__device__ __forceinline__ uint64_t fresh(uint64_t desc, int count) { return desc + (uint32_t)(count >> 30); }
+
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -154,183 +159,184 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (warp == 10) {
-        // ---------------------------------------------------------------- scheduler
+    // (one instruction a warpgroup, ahead of the roles: setmaxnreg is .aligned)
+    if (warp >= 8) {
         setmaxnreg_dec<kOtherRegs>();
-        const int per_z = slots * a.Hk;
-        AttnOrder order;
-        if constexpr (PACKED) order.init(a, 2 * R);
-        feed.run([&](int u, Item &it) -> bool {
-            it.z = u / per_z;
-            const int rest = u - it.z * per_z;
-            it.hk = rest % a.Hk;
-            AttnTile t;
-            if (PACKED && order.on) {
-                if (!order.locate(a, rest / a.Hk, 2 * R, t)) return false;
-            } else {
-                // heaviest first: a causal sequence's last rows see the most keys
-                int64_t slot = slots - 1 - rest / a.Hk;
-                if (!PACKED) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
-                if (!attn_locate(a, true, slot, 1, 2 * R, t)) return false;
-            }
-            const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
-            it.keys = (int)(ke > kb ? ke - kb : 0);
-            it.q_tok = (int)(t.q0 + t.row0);
-            it.q_left = (int)(t.tq - t.row0);
-            it.k_tok = (int)(t.k0 + kb);
-            it.k_left = (int)(t.tk - kb);
-            it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX - 512), -(int64_t)INT_MAX / 2);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
-                const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
-                it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
-            }
-            it.n = max(it.nt[0], it.nt[1]);
-            return true;
-        });
-    } else if (warp == 8) {
-        // ---------------------------------------------------------------- TMA producer
-        setmaxnreg_dec<kOtherRegs>();
-        const uint32_t qbytes = (uint32_t)(R * a.G) * 128u * C::NG;
-        Item it;
-        int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
-        bool ok = true;
-        while (ok && feed.take(ni, it)) {
-            if (lane == 0) {
-                auto load_q = [&](int w) {
-                    if (it.nt[w] == 0) return true;
-                    if (nq[w] > 0 && !mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag)) return false;
-                    mbar_arrive_expect_tx(&full_q[w], qbytes);
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, it.hk * a.G,
-                                    it.q_tok + w * R);
-                    ++nq[w];
-                    return true;
-                };
-                ok = load_q(0);
-                for (int j = 0; ok && j < it.n; ++j) {
-                    const int st = kv & 1;
-                    const uint32_t ph = ((kv >> 1) - 1) & 1;
-                    if (kv >= 2 && !(ok = mbar_wait_idle(&empty_k[st], ph, abort_flag))) break;
-                    mbar_arrive_expect_tx(&full_k[st], C::T);
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, it.hk,
-                                    it.k_tok + j * kTile);
-                    ++kv;
-                    if (j == 0 && !(ok = load_q(1))) break;
-                    if (nv >= 2 && !(ok = mbar_wait_idle(&empty_v[st], ph, abort_flag))) break;
-                    mbar_arrive_expect_tx(&full_v[st], C::T);
-                    for (int g = 0; g < C::NG; ++g)
-                        tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, it.hk,
-                                    it.k_tok + j * kTile);
-                    ++nv;
+        if (warp == 10) {
+            // ---------------------------------------------------------------- scheduler
+            const int per_z = slots * a.Hk;
+            AttnOrder order;
+            if constexpr (PACKED) order.init(a, 2 * R);
+            feed.run([&](int u, Item &it) -> bool {
+                it.z = u / per_z;
+                const int rest = u - it.z * per_z;
+                it.hk = rest % a.Hk;
+                AttnTile t;
+                if (PACKED && order.on) {
+                    if (!order.locate(a, rest / a.Hk, 2 * R, t)) return false;
+                } else {
+                    // heaviest first: a causal sequence's last rows see the most keys
+                    int64_t slot = slots - 1 - rest / a.Hk;
+                    if (!PACKED) slot = (slot % a.N) * (slots / a.N) + slot / a.N;
+                    if (!attn_locate(a, true, slot, 1, 2 * R, t)) return false;
                 }
-            }
-            if (lane == 0) mbar_arrive(feed.want);
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        }
-        if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA exits
-            for (int w = 0; w < 2; ++w)
-                if (nq[w] > 0) mbar_drain(&full_q[w], (nq[w] - 1) & 1);
-            for (int i = max(0, kv - 2); i < kv; ++i) mbar_drain(&full_k[i & 1], (i >> 1) & 1);
-            for (int i = max(0, nv - 2); i < nv; ++i) mbar_drain(&full_v[i & 1], (i >> 1) & 1);
-        }
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- MMA issuer
-        setmaxnreg_dec<kOtherRegs>();
-        const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
-        const int nk = (a.D + 15) / 16;  // 16-column steps of a head (zeros past D)
-        const uint32_t idO = idesc_bf16_f32(128, 16 * nk, false, true);
-        const uint32_t sbase = smem_u32(sm);
-        const uint64_t qd = kdesc(sbase + C::Q0), kd = kdesc(sbase + C::K0);
-        const uint64_t vd = sdesc(sbase + C::V0, kRegion, 1024, 2);
-        // (the lanes poll as one; all_wait's vote here: 446 -> 464 us at 8192 tokens of 32 heads)
-        auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
-        Item it;
-        int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-        bool ok = true;
-        while (ok && feed.take(ni, it)) {
-            // the same in every lane; the reduction leaves them in uniform registers, from which
-            // the products' descriptors are formed without a move per operand
-            const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
-            const int n = max(nt[0], nt[1]);
-            for (int j = -1; ok && j < n; ++j) {
-                const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
-                const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
-                if (j >= 0) {
-                    if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
-                    const int valid = it.k_left - j * kTile;
-                    if (valid < kTile) {
-                        // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
-                        for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
-                            const int r = (i >> 3) & (kTile - 1);
-                            if (r >= valid)
-                                *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion + r * 128 +
-                                                           (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
-                if (j + 1 < n && !(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
-                const bool second = j < 0 ? nt[1] > 0 : j < nt[1];  // row tile 1 has products here
-#pragma unroll
+                const int64_t kb = it.z * a.split, ke = min64(t.tk, kb + a.split);
+                it.keys = (int)(ke > kb ? ke - kb : 0);
+                it.q_tok = (int)(t.q0 + t.row0);
+                it.q_left = (int)(t.tq - t.row0);
+                it.k_tok = (int)(t.k0 + kb);
+                it.k_left = (int)(t.tk - kb);
+                it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX - 512), -(int64_t)INT_MAX / 2);
+    #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    if (!ok) break;
-                    const bool pv = j >= 0 && j < nt[w], more = j + 1 < nt[w];
-                    if (pv) {
-                        if (!(ok = wait(&b_pa[w], np[w] & 1))) break;
+                    const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
+                    const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
+                    it.nt[w] = lim > 0 ? (lim + kTile - 1) / kTile : 0;
+                }
+                it.n = max(it.nt[0], it.nt[1]);
+                return true;
+            });
+        } else if (warp == 8) {
+            // ---------------------------------------------------------------- TMA producer
+            const uint32_t qbytes = (uint32_t)(R * a.G) * 128u * C::NG;
+            Item it;
+            int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
+            bool ok = true;
+            while (ok && feed.take(ni, it)) {
+                if (lane == 0) {
+                    auto load_q = [&](int w) {
+                        if (it.nt[w] == 0) return true;
+                        if (nq[w] > 0 && !mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag)) return false;
+                        mbar_arrive_expect_tx(&full_q[w], qbytes);
+                        for (int g = 0; g < C::NG; ++g)
+                            tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, it.hk * a.G,
+                                        it.q_tok + w * R);
+                        ++nq[w];
+                        return true;
+                    };
+                    ok = load_q(0);
+                    for (int j = 0; ok && j < it.n; ++j) {
+                        const int st = kv & 1;
+                        const uint32_t ph = ((kv >> 1) - 1) & 1;
+                        if (kv >= 2 && !(ok = mbar_wait_idle(&empty_k[st], ph, abort_flag))) break;
+                        mbar_arrive_expect_tx(&full_k[st], C::T);
+                        for (int g = 0; g < C::NG; ++g)
+                            tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, it.hk,
+                                        it.k_tok + j * kTile);
+                        ++kv;
+                        if (j == 0 && !(ok = load_q(1))) break;
+                        if (nv >= 2 && !(ok = mbar_wait_idle(&empty_v[st], ph, abort_flag))) break;
+                        mbar_arrive_expect_tx(&full_v[st], C::T);
+                        for (int g = 0; g < C::NG; ++g)
+                            tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, it.hk,
+                                        it.k_tok + j * kTile);
+                        ++nv;
+                    }
+                }
+                if (lane == 0) mbar_arrive(feed.want);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            }
+            if (lane == 0 && *abort_flag) {  // let the copies in flight land before the CTA exits
+                for (int w = 0; w < 2; ++w)
+                    if (nq[w] > 0) mbar_drain(&full_q[w], (nq[w] - 1) & 1);
+                for (int i = max(0, kv - 2); i < kv; ++i) mbar_drain(&full_k[i & 1], (i >> 1) & 1);
+                for (int i = max(0, nv - 2); i < nv; ++i) mbar_drain(&full_v[i & 1], (i >> 1) & 1);
+            }
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- MMA issuer
+            const uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+            const int nk = (a.D + 15) / 16;  // 16-column steps of a head (zeros past D)
+            const uint32_t idO = idesc_bf16_f32(128, 16 * nk, false, true);
+            const uint32_t sbase = smem_u32(sm);
+            const uint64_t qd = kdesc(sbase + C::Q0), kd = kdesc(sbase + C::K0);
+            const uint64_t vd = sdesc(sbase + C::V0, kRegion, 1024, 2);
+            // (the lanes poll as one; all_wait's vote here: 446 -> 464 us at 8192 tokens of 32 heads)
+            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+            Item it;
+            int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+            bool ok = true;
+            while (ok && feed.take(ni, it)) {
+                // the same in every lane; the reduction leaves them in uniform registers, from which
+                // the products' descriptors are formed without a move per operand
+                const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
+                const int n = max(nt[0], nt[1]);
+                for (int j = -1; ok && j < n; ++j) {
+                    const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
+                    const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
+                    if (j >= 0) {
+                        if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
+                        const int valid = it.k_left - j * kTile;
+                        if (valid < kTile) {
+                            // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
+                            for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
+                                const int r = (i >> 3) & (kTile - 1);
+                                if (r >= valid)
+                                    *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion + r * 128 +
+                                                               (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (j + 1 < n && !(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
+                    const bool second = j < 0 ? nt[1] > 0 : j < nt[1];  // row tile 1 has products here
+    #pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (!ok) break;
+                        const bool pv = j >= 0 && j < nt[w], more = j + 1 < nt[w];
+                        if (pv) {
+                            if (!(ok = wait(&b_pa[w], np[w] & 1))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+    #pragma unroll
+                                for (int jj = 0; jj < 6; ++jj)
+                                    mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
+                                                    desc_at(v0, jj * 2048), idO, (j > 0 || jj > 0) ? 1u : 0u);
+                            }
+                            __syncwarp();
+                            if (!(ok = wait(&b_pb[w], np[w] & 1))) break;
+                            ++np[w];
+                        }
+                        if (j < 0 && more) {
+                            if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
+                            ++nq[w];
+                        }
                         tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int jj = 0; jj < 6; ++jj)
-                                mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
-                                                desc_at(v0, jj * 2048), idO, (j > 0 || jj > 0) ? 1u : 0u);
+                        // the rest of P V and the next scores without a pause: the pipe holds few products
+                        if ((pv || more) && elect_one()) {
+                            if (pv) {
+    #pragma unroll
+                                for (int jj = 6; jj < 8; ++jj)
+                                    mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
+                                                    desc_at(v0, jj * 2048), idO, 1u);
+                                if (!more) mma_commit(&b_o[w]);
+                            }
+                            if (more) {
+                                const uint64_t q1 = fresh(desc_at(qd, w * C::T), c1);
+    #pragma unroll
+                                for (int kk = 0; kk < DP / 16; ++kk)
+                                    if (kk < nk)
+                                        mma_bf16(tmem + w * 128, desc_at(q1, (kk >> 2) * kRegion + (kk & 3) * 32),
+                                                 desc_at(k1, (kk >> 2) * kRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+                                mma_commit(&b_s[w]);
+                                if (j + 1 == nt[w] - 1) mma_commit(&empty_q[w]);
+                            }
+                            if (w == 1 || !second) {  // the last products of this pair of tiles
+                                if (j >= 0) mma_commit(&empty_v[c0 & 1]);
+                                if (j + 1 < n) mma_commit(&empty_k[c1 & 1]);
+                            }
                         }
                         __syncwarp();
-                        if (!(ok = wait(&b_pb[w], np[w] & 1))) break;
-                        ++np[w];
                     }
-                    if (j < 0 && more) {
-                        if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
-                        ++nq[w];
-                    }
-                    tc_fence_after();
-                    // the rest of P V and the next scores without a pause: the pipe holds few products
-                    if ((pv || more) && elect_one()) {
-                        if (pv) {
-#pragma unroll
-                            for (int jj = 6; jj < 8; ++jj)
-                                mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
-                                                desc_at(v0, jj * 2048), idO, 1u);
-                            if (!more) mma_commit(&b_o[w]);
-                        }
-                        if (more) {
-                            const uint64_t q1 = desc_at(qd, w * C::T);
-#pragma unroll
-                            for (int kk = 0; kk < DP / 16; ++kk)
-                                if (kk < nk)
-                                    mma_bf16(tmem + w * 128, desc_at(q1, (kk >> 2) * kRegion + (kk & 3) * 32),
-                                             desc_at(k1, (kk >> 2) * kRegion + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                            mma_commit(&b_s[w]);
-                            if (j + 1 == nt[w] - 1) mma_commit(&empty_q[w]);
-                        }
-                        if (w == 1 || !second) {  // the last products of this pair of tiles
-                            if (j >= 0) mma_commit(&empty_v[c0 & 1]);
-                            if (j + 1 < n) mma_commit(&empty_k[c1 & 1]);
-                        }
-                    }
-                    __syncwarp();
                 }
+                kv += n;
             }
-            kv += n;
+            if (elect_one()) {
+                mma_commit(b_drain);
+                mbar_drain(b_drain, 0);
+            }
         }
-        if (elect_one()) {
-            mma_commit(b_drain);
-            mbar_drain(b_drain, 0);
-        }
-    } else if (warp < 8) {
+    } else {
         // ---------------------------------------------------------------- softmax: one row a thread
         setmaxnreg_inc<kRowRegs>();
         const int w = warp >> 2, r = threadIdx.x & 127;
@@ -448,8 +454,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             tc_fence_before();  // the next item's first product overwrites O after its P arrives
         }
         if (*abort_flag && a.status) atomicExch(a.status, kDevTimeout);
-    } else {
-        setmaxnreg_dec<kOtherRegs>();
     }
     __syncwarp();
     tc_fence_before();

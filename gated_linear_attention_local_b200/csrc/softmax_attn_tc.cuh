@@ -7,9 +7,10 @@
 namespace sgla {
 namespace {
 
-// Registers a thread of a 384-thread kernel: 168 at launch; its eight row warps take 224, the
-// others keep 48 (256 * 224 + 128 * 48 = 63488 of 384 * 168 = 64512).
-constexpr int kRowRegs = 224, kOtherRegs = 48;
+// Registers a thread of a 384-thread kernel: 168 at launch; its eight row warps take 216, the
+// others keep 72 (256 * 216 + 128 * 72 = 64512 = 384 * 168).  With 224 and 56 the product warps spill
+// (dk dv of 2 x 4096 tokens, 16 heads on 4: 254 us for 231).
+constexpr int kRowRegs = 216, kOtherRegs = 72;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Exponentials on the FMA pipe: with n = round(x), f = x - n, 2^x = 2^n p3(f), p3 the degree-3
