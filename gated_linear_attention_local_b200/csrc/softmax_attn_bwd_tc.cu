@@ -609,8 +609,11 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
             const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
             const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
-            // (the lanes poll as one; all_wait's vote here: 177 -> 180 us at 2 x 4096 tokens of 16 heads)
-            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+            // A wait that gave up turns the lane's later ones off, and products are issued only while
+            // the elected lane's have all come through; the lanes stay together to the item's end, where
+            // they vote (a vote on every wait, all_wait: 177 -> 180 us at 2 x 4096 tokens of 16 heads).
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && mbar_wait(bar, ph, abort_flag); };
             QItem it;
             int ni = 0;
             uint32_t own_ph = 0;
@@ -618,22 +621,21 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             Ring<kStY> y1;
             Ring<2> d1, d0;     // dP's buffers, of the scores' tile, of the sum's tile
             uint32_t free_ph = 1;  // parity of S's release by the tile before the scores' tile
-            bool ok = true;
-            while (ok && feed.take(ni, it)) {
+            while (__all_sync(0xffffffffu, ok) && feed.take(ni, it)) {
                 const int n = __reduce_max_sync(0xffffffffu, it.n);
                 if (n == 0) continue;
-                if (!(ok = wait(b.own, own_ph))) break;
+                wait(b.own, own_ph);
                 own_ph ^= 1u;
-                for (int i = -1; ok && i < n; ++i) {
+                for (int i = -1; i < n; ++i) {
                     if (i + 1 < n) {
-                        if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
+                        wait(&b.full_x[x1.s], x1.ph);
                         const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
                         if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
-                        if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
-                        if (!(ok = wait(b.sfree, free_ph))) break;  // (the very first passes at once)
+                        wait(&b.full_y[y1.s], y1.ph);
+                        wait(b.sfree, free_ph);  // (the very first passes at once)
                         free_ph ^= 1u;
                         tc_fence_after();
-                        if (elect_one()) {
+                        if (elect_one() && ok) {
                             issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
                             mma_commit(b.s);
                             issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
@@ -647,9 +649,9 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         d1.step();
                     }
                     if (i >= 0) {
-                        if (!(ok = wait(&b.ds[d0.s], d0.ph))) break;
+                        wait(&b.ds[d0.s], d0.ph);
                         tc_fence_after();
-                        if (elect_one()) {
+                        if (elect_one() && ok) {
                             issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + d0.s * 128, desc_at(xm, x0.s * C::T), idA,
                                       i > 0);
                             mma_commit(&b.empty_x[x0.s]);

@@ -187,7 +187,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 it.k_tok = (int)(t.k0 + kb);
                 it.k_left = (int)(t.tk - kb);
                 it.shift = (int)max(min64(t.row0 + t.tk - t.tq - kb, (int64_t)INT_MAX - 512), -(int64_t)INT_MAX / 2);
-    #pragma unroll
+#pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const int last = min((w + 1) * R, it.q_left) - 1;  // last token of the row tile
                     const int lim = w * R >= it.q_left ? 0 : (a.causal ? min(it.keys, last + 1 + it.shift) : it.keys);
@@ -250,27 +250,29 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const uint32_t sbase = smem_u32(sm);
             const uint64_t qd = kdesc(sbase + C::Q0), kd = kdesc(sbase + C::K0);
             const uint64_t vd = sdesc(sbase + C::V0, kRegion, 1024, 2);
-            // (the lanes poll as one; all_wait's vote here: 446 -> 464 us at 8192 tokens of 32 heads)
-            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait(bar, ph, abort_flag); };
+            // A wait that gave up turns the lane's later ones off, and products are issued only while
+            // the elected lane's have all come through; the lanes stay together to the item's end, where
+            // they vote (a vote on every wait, all_wait: 446 -> 464 us at 8192 tokens of 32 heads).
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && mbar_wait(bar, ph, abort_flag); };
             Item it;
             int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            bool ok = true;
-            while (ok && feed.take(ni, it)) {
+            while (__all_sync(0xffffffffu, ok) && feed.take(ni, it)) {
                 // the same in every lane; the reduction leaves them in uniform registers, from which
                 // the products' descriptors are formed without a move per operand
                 const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
                 const int n = max(nt[0], nt[1]);
-                for (int j = -1; ok && j < n; ++j) {
+                for (int j = -1; j < n; ++j) {
                     const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
                     const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
                     if (j >= 0) {
-                        if (!(ok = wait(&full_v[c0 & 1], (c0 >> 1) & 1))) break;
+                        wait(&full_v[c0 & 1], (c0 >> 1) & 1);
                         const int valid = it.k_left - j * kTile;
                         if (valid < kTile) {
                             // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
                             for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
                                 const int r = (i >> 3) & (kTile - 1);
-                                if (r >= valid)
+                                if (ok && r >= valid)
                                     *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion + r * 128 +
                                                                (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                             }
@@ -278,34 +280,33 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             __syncwarp();
                         }
                     }
-                    if (j + 1 < n && !(ok = wait(&full_k[c1 & 1], (c1 >> 1) & 1))) break;
+                    if (j + 1 < n) wait(&full_k[c1 & 1], (c1 >> 1) & 1);
                     const bool second = j < 0 ? nt[1] > 0 : j < nt[1];  // row tile 1 has products here
-    #pragma unroll
+#pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        if (!ok) break;
                         const bool pv = j >= 0 && j < nt[w], more = j + 1 < nt[w];
                         if (pv) {
-                            if (!(ok = wait(&b_pa[w], np[w] & 1))) break;
+                            wait(&b_pa[w], np[w] & 1);
                             tc_fence_after();
-                            if (elect_one()) {
-    #pragma unroll
+                            if (elect_one() && ok) {
+#pragma unroll
                                 for (int jj = 0; jj < 6; ++jj)
                                     mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
                                                     desc_at(v0, jj * 2048), idO, (j > 0 || jj > 0) ? 1u : 0u);
                             }
                             __syncwarp();
-                            if (!(ok = wait(&b_pb[w], np[w] & 1))) break;
+                            wait(&b_pb[w], np[w] & 1);
                             ++np[w];
                         }
                         if (j < 0 && more) {
-                            if (!(ok = wait(&full_q[w], nq[w] & 1))) break;
+                            wait(&full_q[w], nq[w] & 1);
                             ++nq[w];
                         }
                         tc_fence_after();
                         // the rest of P V and the next scores without a pause: the pipe holds few products
-                        if ((pv || more) && elect_one()) {
+                        if ((pv || more) && elect_one() && ok) {
                             if (pv) {
-    #pragma unroll
+#pragma unroll
                                 for (int jj = 6; jj < 8; ++jj)
                                     mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
                                                     desc_at(v0, jj * 2048), idO, 1u);
@@ -313,7 +314,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             }
                             if (more) {
                                 const uint64_t q1 = fresh(desc_at(qd, w * C::T), c1);
-    #pragma unroll
+#pragma unroll
                                 for (int kk = 0; kk < DP / 16; ++kk)
                                     if (kk < nk)
                                         mma_bf16(tmem + w * 128, desc_at(q1, (kk >> 2) * kRegion + (kk & 3) * 32),
