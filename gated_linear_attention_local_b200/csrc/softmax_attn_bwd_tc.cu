@@ -208,21 +208,23 @@ __device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, con
     Ring<kStX> rx;
     Ring<kStY> ry;
     bool ok = true;
+    // (what a product warp that gave up released is not filled again)
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait_idle(bar, ph, abort_flag) && !*abort_flag; };
     while (ok && feed.take(ni, it)) {
         if (lane == 0 && it.n > 0) {
-            if (no > 0) ok = mbar_wait_idle(b.empty_own, (no - 1) & 1, abort_flag);
+            if (no > 0) ok = wait(b.empty_own, (no - 1) & 1);
             if (ok) {
                 mbar_arrive_expect_tx(b.own, own_bytes);
                 own(it, b.own);
                 ++no;
             }
             for (int i = 0; ok && i < it.n; ++i) {
-                if (nx >= kStX && !(ok = mbar_wait_idle(&b.empty_x[rx.s], rx.ph ^ 1u, abort_flag))) break;
+                if (nx >= kStX && !(ok = wait(&b.empty_x[rx.s], rx.ph ^ 1u))) break;
                 mbar_arrive_expect_tx(&b.full_x[rx.s], bytes);
                 x(it, i, sm + C::X0 + rx.s * C::T, &b.full_x[rx.s]);
                 rx.step();
                 ++nx;
-                if (ny >= kStY && !(ok = mbar_wait_idle(&b.empty_y[ry.s], ry.ph ^ 1u, abort_flag))) break;
+                if (ny >= kStY && !(ok = wait(&b.empty_y[ry.s], ry.ph ^ 1u))) break;
                 mbar_arrive_expect_tx(&b.full_y[ry.s], bytes);
                 y(it, i, sm + C::Y0 + ry.s * C::T, &b.full_y[ry.s]);
                 ry.step();
@@ -609,11 +611,11 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const uint64_t qd = kdesc(sbase + C::A0), dd = kdesc(sbase + C::B0);
             const uint64_t xk = kdesc(sbase + C::X0), yk = kdesc(sbase + C::Y0);
             const uint64_t xm = sdesc(sbase + C::X0, kRegion, 1024, 2);
-            // A wait that gave up turns the lane's later ones off, and products are issued only while
-            // the elected lane's have all come through; the lanes stay together to the item's end, where
-            // they vote (a vote on every wait, all_wait: 177 -> 180 us at 2 x 4096 tokens of 16 heads).
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && mbar_wait(bar, ph, abort_flag); };
+            // A wait that gave up (abort is set then) sends no lane another way: the products go on, over
+            // whatever is there, to the item's end, where the lanes vote.  (A vote on every wait, all_wait:
+            // 177 -> 180 us at 2 x 4096 tokens of 16 heads.)
+            auto wait = [&](uint64_t *bar, uint32_t ph) { mbar_wait(bar, ph, abort_flag); };
+            auto sound = [&] { return __all_sync(0xffffffffu, !*abort_flag); };
             QItem it;
             int ni = 0;
             uint32_t own_ph = 0;
@@ -621,12 +623,13 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             Ring<kStY> y1;
             Ring<2> d1, d0;     // dP's buffers, of the scores' tile, of the sum's tile
             uint32_t free_ph = 1;  // parity of S's release by the tile before the scores' tile
-            while (__all_sync(0xffffffffu, ok) && feed.take(ni, it)) {
+            while (sound() && feed.take(ni, it)) {
                 const int n = __reduce_max_sync(0xffffffffu, it.n);
                 if (n == 0) continue;
                 wait(b.own, own_ph);
                 own_ph ^= 1u;
                 for (int i = -1; i < n; ++i) {
+                    if ((i & 1023) == 1023 && i > 0 && !sound()) break;  // (the rest of a long item)
                     if (i + 1 < n) {
                         wait(&b.full_x[x1.s], x1.ph);
                         const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
@@ -635,7 +638,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                         wait(b.sfree, free_ph);  // (the very first passes at once)
                         free_ph ^= 1u;
                         tc_fence_after();
-                        if (elect_one() && ok) {
+                        if (elect_one()) {
                             issue_scores<DP>(tmem + C::COL_S, qd, desc_at(xk, x1.s * C::T), idS, nk);
                             mma_commit(b.s);
                             issue_scores<DP>(tmem + C::COL_DP + d1.s * 128, dd, desc_at(yk, y1.s * C::T), idS, nk);
@@ -651,7 +654,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     if (i >= 0) {
                         wait(&b.ds[d0.s], d0.ph);
                         tc_fence_after();
-                        if (elect_one() && ok) {
+                        if (elect_one()) {
                             issue_sum(tmem + C::COL_ACC + 128, tmem + C::COL_DP + d0.s * 128, desc_at(xm, x0.s * C::T), idA,
                                       i > 0);
                             mma_commit(&b.empty_x[x0.s]);

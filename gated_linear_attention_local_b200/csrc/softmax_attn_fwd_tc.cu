@@ -202,11 +202,13 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             Item it;
             int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
             bool ok = true;
+            // (what a product warp that gave up released is not filled again)
+            auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait_idle(bar, ph, abort_flag) && !*abort_flag; };
             while (ok && feed.take(ni, it)) {
                 if (lane == 0) {
                     auto load_q = [&](int w) {
                         if (it.nt[w] == 0) return true;
-                        if (nq[w] > 0 && !mbar_wait_idle(&empty_q[w], (nq[w] - 1) & 1, abort_flag)) return false;
+                        if (nq[w] > 0 && !wait(&empty_q[w], (nq[w] - 1) & 1)) return false;
                         mbar_arrive_expect_tx(&full_q[w], qbytes);
                         for (int g = 0; g < C::NG; ++g)
                             tma_load_3d(sm + C::Q0 + w * C::T + g * kRegion, &tq, &full_q[w], 64 * g, it.hk * a.G,
@@ -218,14 +220,14 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                     for (int j = 0; ok && j < it.n; ++j) {
                         const int st = kv & 1;
                         const uint32_t ph = ((kv >> 1) - 1) & 1;
-                        if (kv >= 2 && !(ok = mbar_wait_idle(&empty_k[st], ph, abort_flag))) break;
+                        if (kv >= 2 && !(ok = wait(&empty_k[st], ph))) break;
                         mbar_arrive_expect_tx(&full_k[st], C::T);
                         for (int g = 0; g < C::NG; ++g)
                             tma_load_3d(sm + C::K0 + st * C::T + g * kRegion, &tk, &full_k[st], 64 * g, it.hk,
                                         it.k_tok + j * kTile);
                         ++kv;
                         if (j == 0 && !(ok = load_q(1))) break;
-                        if (nv >= 2 && !(ok = mbar_wait_idle(&empty_v[st], ph, abort_flag))) break;
+                        if (nv >= 2 && !(ok = wait(&empty_v[st], ph))) break;
                         mbar_arrive_expect_tx(&full_v[st], C::T);
                         for (int g = 0; g < C::NG; ++g)
                             tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, it.hk,
@@ -250,19 +252,20 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const uint32_t sbase = smem_u32(sm);
             const uint64_t qd = kdesc(sbase + C::Q0), kd = kdesc(sbase + C::K0);
             const uint64_t vd = sdesc(sbase + C::V0, kRegion, 1024, 2);
-            // A wait that gave up turns the lane's later ones off, and products are issued only while
-            // the elected lane's have all come through; the lanes stay together to the item's end, where
-            // they vote (a vote on every wait, all_wait: 446 -> 464 us at 8192 tokens of 32 heads).
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t ph) { ok = ok && mbar_wait(bar, ph, abort_flag); };
+            // A wait that gave up (abort is set then) sends no lane another way: the products go on, over
+            // whatever is there, to the item's end, where the lanes vote.  (A vote on every wait, all_wait:
+            // 446 -> 464 us at 8192 tokens of 32 heads.)
+            auto wait = [&](uint64_t *bar, uint32_t ph) { mbar_wait(bar, ph, abort_flag); };
+            auto sound = [&] { return __all_sync(0xffffffffu, !*abort_flag); };
             Item it;
             int ni = 0, kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            while (__all_sync(0xffffffffu, ok) && feed.take(ni, it)) {
+            while (sound() && feed.take(ni, it)) {
                 // the same in every lane; the reduction leaves them in uniform registers, from which
                 // the products' descriptors are formed without a move per operand
                 const int nt[2] = {__reduce_max_sync(0xffffffffu, it.nt[0]), __reduce_max_sync(0xffffffffu, it.nt[1])};
                 const int n = max(nt[0], nt[1]);
                 for (int j = -1; j < n; ++j) {
+                    if ((j & 1023) == 1023 && j > 0 && !sound()) break;  // (the rest of a long item)
                     const int c0 = kv + j, c1 = kv + j + 1;  // ring positions of key tiles j and j + 1
                     const uint64_t v0 = desc_at(vd, (c0 & 1) * C::T), k1 = desc_at(kd, (c1 & 1) * C::T);
                     if (j >= 0) {
@@ -272,7 +275,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                             // rows behind the sequence's keys hold its neighbour's data: 0 * NaN must not arise
                             for (int i = lane; i < C::NG * 8 * kTile; i += 32) {
                                 const int r = (i >> 3) & (kTile - 1);
-                                if (ok && r >= valid)
+                                if (r >= valid)
                                     *reinterpret_cast<uint4 *>(sm + C::V0 + (c0 & 1) * C::T + (i >> 10) * kRegion + r * 128 +
                                                                (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                             }
@@ -288,7 +291,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         if (pv) {
                             wait(&b_pa[w], np[w] & 1);
                             tc_fence_after();
-                            if (elect_one() && ok) {
+                            if (elect_one()) {
 #pragma unroll
                                 for (int jj = 0; jj < 6; ++jj)
                                     mma_bf16_tmem_a(tmem + C::COL_O + w * 128, tmem + w * 128 + jj * 8,
@@ -304,7 +307,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         }
                         tc_fence_after();
                         // the rest of P V and the next scores without a pause: the pipe holds few products
-                        if ((pv || more) && elect_one() && ok) {
+                        if ((pv || more) && elect_one()) {
                             if (pv) {
 #pragma unroll
                                 for (int jj = 6; jj < 8; ++jj)

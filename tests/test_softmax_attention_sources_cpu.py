@@ -50,9 +50,11 @@ def test_registers_move_for_whole_warpgroups(name):
 
 @pytest.mark.parametrize("name", sorted(KERNELS))
 def test_no_wait_sends_lanes_different_ways(name):
-    """A bounded wait can end differently in the lanes of a warp.  Either the warp votes (all_wait), or the answer only
-    turns later waits off: a lane that left a loop on its own answer would leave others at a warp-wide instruction."""
-    for m in re.finditer(r"[^;{}]*\bmbar_wait\(", KERNELS[name]):
-        assert re.match(r"\s*ok = ok && mbar_wait", m.group(0)), m.group(0).strip()
-    if "auto wait" in KERNELS[name]:
-        assert re.search(r"auto wait = \[&\]\([^)]*\) \{ (return all_wait|ok = ok && mbar_wait)\(", KERNELS[name])
+    """A bounded wait can end differently in the lanes of a warp, and a lane that left a loop on its own answer would
+    leave others at a warp-wide instruction.  So the warp votes (all_wait), or the answer is dropped (the abort flag
+    says it to the item's end), or it only turns the lane's later waits off."""
+    uses = re.findall(r"[^;{}]*[;{}]?[^;{}]*\bmbar_wait\(", KERNELS[name])
+    assert uses
+    for use in uses:
+        assert re.search(r"(ok = ok && |auto wait = \[&\]\([^)]*\) \{ )mbar_wait\($", use), use.strip()
+    assert re.search(r"auto wait = \[&\]\([^)]*\) \{ (return all_wait|mbar_wait)\(", KERNELS[name])
