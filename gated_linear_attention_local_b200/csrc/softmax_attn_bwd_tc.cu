@@ -65,7 +65,7 @@ struct BwdCfg {
     static constexpr uint32_t X0 = 2 * T, Y0 = X0 + kStX * T;
     static constexpr uint32_t ROWS = Y0 + kStY * T;  // [2][128] -lse (log2 units), [128] -delta of a tile's rows
     static constexpr uint32_t BARS = ROWS + 2 * 256 * 4;
-    static constexpr uint32_t MISC = BARS + 26 * 8;  // tensor memory address, abort flag, 16 bytes of the feed
+    static constexpr uint32_t MISC = BARS + 26 * 8;  // tensor memory address, abort flag, copies so far, 16 bytes of the feed
     static constexpr uint32_t ITEM = MISC + 32;
     // (no slack for alignment: the array is declared with it)
     static constexpr size_t SMEM = ITEM + 64 > 120 * 1024 ? ITEM + 64 : 120 * 1024;
@@ -228,7 +228,7 @@ __device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, con
                 mbar_arrive_expect_tx(&b.full_y[ry.s], bytes);
                 y(it, i, sm + C::Y0 + ry.s * C::T, &b.full_y[ry.s]);
                 ry.step();
-                ++ny;
+                *feed.copies = ++ny;
             }
         }
         if (lane == 0) mbar_arrive(feed.want);
@@ -282,7 +282,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
     const Feed<KvItem> feed{b.feed, b.feed + 1, b.feed + 2, b.feed + 3, sm + C::MISC + 16, reinterpret_cast<KvItem *>(sm + C::ITEM),
-                            abort_flag};
+                            abort_flag, abort_flag + 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 256) {
         prefetch_tmap(&tq);
@@ -293,7 +293,6 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
     if (threadIdx.x == 0) {
         b.init();
         feed.init();
-        *abort_flag = 0;
         mbar_fence_init();
     }
     if (R * a.G < kTile && warp < kStX + kStY)  // rows that no copy writes are operands too
@@ -541,7 +540,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
     const Feed<QItem> feed{b.feed, b.feed + 1, b.feed + 2, b.feed + 3, sm + C::MISC + 16, reinterpret_cast<QItem *>(sm + C::ITEM),
-                           abort_flag};
+                           abort_flag, abort_flag + 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 256) {
         prefetch_tmap(&tq);
@@ -552,7 +551,6 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
     if (threadIdx.x == 0) {
         b.init();
         feed.init();
-        *abort_flag = 0;
         mbar_fence_init();
     }
     if (warp == 9) {

@@ -133,7 +133,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + C::MISC + 8);
     const Feed<Item> feed{bars + 20, bars + 21, bars + 22, bars + 24, sm + C::MISC + 16, reinterpret_cast<Item *>(sm + C::ITEM),
-                          abort_flag};
+                          abort_flag, abort_flag + 1};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int b = 0; b < 16; ++b) mbar_init(&bars[b], 1);
@@ -143,7 +143,6 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         feed.init();
         mbar_init(b_drain, 1);
-        *abort_flag = 0;
         mbar_fence_init();
     }
     if (threadIdx.x == 256) {
@@ -232,7 +231,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         for (int g = 0; g < C::NG; ++g)
                             tma_load_3d(sm + C::V0 + st * C::T + g * kRegion, &tv, &full_v[st], 64 * g, it.hk,
                                         it.k_tok + j * kTile);
-                        ++nv;
+                        *feed.copies = ++nv;
                     }
                 }
                 if (lane == 0) mbar_arrive(feed.want);

@@ -62,6 +62,30 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+// A wait that lasts as long as an item, and an item may have any number of tiles (a wait for one tile
+// is bounded by itself): gives up when no copy has been issued for the limit, or another thread gave
+// up.  IDLE: off the critical path, sleeps in the barrier.
+template <bool IDLE>
+__device__ __forceinline__ bool item_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, volatile int *copies) {
+    auto poll = [&] { return IDLE ? mbar_try_wait_hint(bar, parity, 20000u) : mbar_try_wait(bar, parity); };
+    if (poll()) return true;
+    uint64_t start = globaltimer_ns();
+    int seen = *copies;
+    while (true) {
+        if (poll()) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - start > kWaitLimitNs) {
+            const int now = *copies;
+            if (now == seen) {
+                *abort_flag = 1;
+                return false;
+            }
+            seen = now;
+            start = globaltimer_ns();
+        }
+    }
+}
+
 // Work items of a kernel whose grid has a block for every item but whose CTAs stay on their SM: a
 // scheduler warp takes over blocks that have not started (clusterlaunchcontrol), describes them
 // and hands the description to the other warps.  It asks when the copies of the item in work
@@ -75,8 +99,11 @@ struct Feed {
     void *answer;                   // 16 bytes, 16-byte aligned
     Item *item;
     volatile int *abort_flag;
+    volatile int *copies;           // tiles copied so far (written by the copying lane)
 
     __device__ void init() const {
+        *abort_flag = 0;
+        *copies = 0;
         mbar_init(full, 1);
         mbar_init(empty, kFeedWarps);
         mbar_init(want, 1);
@@ -84,7 +111,7 @@ struct Feed {
     }
     // The next item, by all lanes of a warp; false when there is none.
     __device__ bool take(int &count, Item &it) const {
-        if (!all_wait(full, count & 1, abort_flag)) return false;
+        if (!__all_sync(0xffffffffu, item_wait<false>(full, count & 1, abort_flag, copies))) return false;
         it = *item;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
@@ -98,7 +125,7 @@ struct Feed {
         int count = 0;
         bool ok = true;
         auto publish = [&](const Item &it) {
-            if (count > 0) ok = __all_sync(0xffffffffu, mbar_wait_idle(empty, (count - 1) & 1, abort_flag));
+            if (count > 0) ok = __all_sync(0xffffffffu, item_wait<true>(empty, (count - 1) & 1, abort_flag, copies));
             if (ok && lane == 0) {
                 *item = it;
                 mbar_arrive(full);
@@ -110,7 +137,7 @@ struct Feed {
             Item it;
             if (describe(u, it)) {
                 publish(it);
-                if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait_idle(want, (count - 1) & 1, abort_flag)))) break;
+                if (!ok || !(ok = __all_sync(0xffffffffu, item_wait<true>(want, (count - 1) & 1, abort_flag, copies)))) break;
             }
             __syncwarp();
             if (lane == 0) {

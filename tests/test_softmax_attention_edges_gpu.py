@@ -1,0 +1,43 @@
+"""Softmax attention at the ends of what its calls allow: very long items, extreme and non-finite values, rows that see
+nothing."""
+import pytest
+import torch
+
+import gated_linear_attention_local_b200 as sg
+
+pytestmark = pytest.mark.gpu
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.init()
+
+
+def test_a_block_of_keys_that_takes_seconds():
+    """128 keys seen by 2^28 rows: one work item of dk dv walks 2^21 tiles (some 4 s), longer than any wait may last
+    without progress.  All scores are 0, so p = 2^-7.
+
+    With every row of do 1, dv sums 2^28 terms of 2^-7.  Multiples of 2^-7 up to 2^17 fit the 24 bits of fp32, so the
+    running sum is exact to there; from there on a term may vanish beside it (an fp32 sum of n terms is only known to
+    n 2^-24 of itself, 16 here), but none lowers it and none is counted for more than it is: 2^17 <= dv <= 2^21.  With
+    do = 1 in the last token alone, dv = 128 2^-7 = 1 exactly, which shows the walk's end."""
+    T, H, S, D = 1 << 21, 128, 128, 8
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    q = torch.zeros(1, T, H, D, device="cuda", dtype=BF16)
+    do = torch.ones_like(q)
+    k = torch.randn(1, S, 1, D, device="cuda", dtype=BF16)
+    v = torch.zeros_like(k)
+    status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    o, lse = sg.softmax_attention_fwd(q, k, v, causal=False, device_status=status)
+    assert int(status) == 0 and float(o.abs().max()) == 0.0
+    r = sg.softmax_attention_bwd(q, k, v, o, lse, do, causal=False, device_status=status)
+    assert int(status) == 0
+    assert 2.0 ** 17 <= float(r["dv"].min()) and float(r["dv"].max()) <= 2.0 ** 21
+    assert float(r["dk"].abs().max()) == 0.0 and float(r["dq"].abs().max()) == 0.0
+    do[:, :-1] = 0
+    r = sg.softmax_attention_bwd(q, k, v, o, lse, do, causal=False, device_status=status)
+    assert int(status) == 0 and bool((r["dv"] == 1.0).all())
