@@ -41,6 +41,7 @@ import functools
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as _lib_mod
 from ._lib import (SGLA_BF16, SGLA_FP32, SGLA_OK, SglaError, lib, library_path,  # noqa: F401
@@ -105,6 +106,17 @@ def _check_cuda(name, t, dtype=None, ndim=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+
+
+def _autograd_follows(*tensors):
+    """Whether a call on these belongs to autograd: one requires a gradient (and gradients are enabled), or carries a
+    forward-mode tangent, which the autograd functions refuse (they have no jvp) and a plain call would drop."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None
+                                                  for t in tensors)
 
 
 def fwd_workspace_size(B, T, H, K, V, chunk_size=64, dtype=torch.bfloat16) -> int:
@@ -393,8 +405,7 @@ def chunk_simple_gla(q, k, v, g=None, g_gamma=None, scale=None, initial_state=No
     given; state_v_first selects the [N,H,V,K] state layout.  When gradients are
     enabled and an input requires them, the call is differentiable (backward through
     simple_gla_chunk_bwd)."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (q, k, v, g, g_gamma, initial_state)):
+    if _autograd_follows(q, k, v, g, g_gamma, initial_state):
         return ChunkSimpleGLAFunction.apply(q, k, v, g, g_gamma, initial_state, scale, output_final_state,
                                             cu_seqlens, chunk_size, state_v_first)
     if state_v_first:

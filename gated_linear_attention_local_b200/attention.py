@@ -15,7 +15,7 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _DTYPES, _check_cuda, _on_tensor_device, _ptr, _scale, _stream, _workspace
+from . import _DTYPES, _autograd_follows, _check_cuda, _on_tensor_device, _ptr, _scale, _stream, _workspace
 from ._lib import SGLA_ERR_WORKSPACE, lib, raise_for_status
 
 __all__ = ["softmax_attention", "softmax_attention_fwd", "softmax_attention_bwd", "softmax_attention_decode_step",
@@ -154,7 +154,7 @@ class SoftmaxAttentionFunction(torch.autograd.Function):
 def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None):
     """The output of softmax_attention_fwd alone; differentiable in q, k and v (through softmax_attention_bwd) when
     gradients are enabled and one of them requires gradients."""
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+    if _autograd_follows(q, k, v):
         return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
     return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, want_lse=False)[0]
 
@@ -274,7 +274,7 @@ def multi_axis_rotary(q, k, positions, inv_freq, axes=None, interleaved=False):
     positions[..., axes[i]] * inv_freq[i].  positions int64 [..., A], or [...] for one axis; inv_freq fp32 [R/2],
     R <= D (later columns pass unchanged); axes: R/2 ints, the axis of each pair (None: axis 0).  Pairs are
     (i, i + R/2), or (2i, 2i + 1) with interleaved.  Returns (q', k'); differentiable in q and k."""
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if _autograd_follows(q, k):
         return MultiAxisRotaryFunction.apply(q, k, positions, inv_freq, axes, interleaved)
     return _rotary(q, k, positions, inv_freq, axes, interleaved, False, "multi_axis_rotary")
 
