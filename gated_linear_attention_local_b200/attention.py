@@ -2,7 +2,8 @@
 transform of q and k in front of either mixer ("relinear -- convert pretrained transformers to linear/hybrid-attention
 models").  Argument marshalling for the entry points of ``include/simple_gla.h``, as in the package's ``__init__``.
 
-  softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None) -> o, differentiable
+  softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None, device_status=None) -> o,
+      differentiable
   softmax_attention_fwd(...) -> (o, lse);  softmax_attention_bwd(q, k, v, o, lse, do, ...) -> {dq, dk, dv}
   softmax_attention_decode_step(q, k_cache, v_cache, lengths, prefix_k=None, prefix_v=None, scale=None) -> o
   multi_axis_rotary(q, k, positions, inv_freq, axes=None, interleaved=False) -> (q, k) rotated, differentiable
@@ -78,11 +79,11 @@ def _attention_shapes(q, k, v, cu_seqlens, cu_seqlens_k):
     return N, qs[-3], ks[-3], H, Hk, D, dt, cu_seqlens_k
 
 
-def _check_status(device_status):
+def _check_status(device_status, words=1):
     if device_status is not None:
         _check_cuda("device_status", device_status, torch.int32)
-        if device_status.numel() < 1:
-            raise ValueError("device_status must hold one element")
+        if device_status.numel() < words:
+            raise ValueError(f"device_status must hold {words} element{'s' if words > 1 else ''}")
 
 
 def _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=None, want_lse=True):
@@ -135,28 +136,32 @@ class SoftmaxAttentionFunction(torch.autograd.Function):
     """softmax_attention_fwd with softmax_attention_bwd as its gradient."""
 
     @staticmethod
-    def forward(ctx, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k):
-        o, lse = _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
+    def forward(ctx, q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status=None):
+        _check_status(device_status, 2)
+        o, lse = _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
-        ctx.opts = (causal, scale)
+        # (written to, never read here: no saved tensor, so that one word may serve many steps)
+        ctx.opts = (causal, scale, None if device_status is None else device_status.flatten()[1:])
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
-        causal, scale = ctx.opts
-        r = softmax_attention_bwd(q, k, v, o, lse, do.contiguous(), causal, scale, cu, cu_k)
-        return r["dq"], r["dk"], r["dv"], None, None, None, None
+        causal, scale, status = ctx.opts
+        r = softmax_attention_bwd(q, k, v, o, lse, do.contiguous(), causal, scale, cu, cu_k, status)
+        return r["dq"], r["dk"], r["dv"], None, None, None, None, None
 
 
 @_on_tensor_device
-def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None):
+def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seqlens_k=None, device_status=None):
     """The output of softmax_attention_fwd alone; differentiable in q, k and v (through softmax_attention_bwd) when
-    gradients are enabled and one of them requires gradients."""
+    gradients are enabled and one of them requires gradients.  device_status: optional int32 CUDA tensor that receives
+    what the device finds (sequences whose bounds are bad are skipped, their outputs and gradients not written): element
+    0 the forward's status, element 1 the gradients' once they run (it is needed when the call is differentiable)."""
     if _autograd_follows(q, k, v):
-        return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k)
-    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, want_lse=False)[0]
+        return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status)
+    return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status, want_lse=False)[0]
 
 
 @_on_tensor_device

@@ -38,3 +38,47 @@ def test_forward_mode_tangents_are_not_dropped(plain, name, which):
             call(*x)
         with torch.no_grad(), pytest.raises(RuntimeError):  # which stops reverse mode only
             call(*x)
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """Stands in for the library: every call succeeds and is recorded with the address of its status word."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return lambda *a: 256
+            where = {"softmax_attention_fwd": 16, "softmax_attention_bwd": 20}[name]
+
+            def call(*a):
+                seen.append((name, a[where]))
+                return 0
+            return call
+    monkeypatch.setattr(attention, "lib", Library)
+    monkeypatch.setattr(attention, "_stream", lambda: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)  # argument checks run, nothing is launched
+    monkeypatch.setattr(attention, "softmax_attention_bwd", sg.softmax_attention_bwd.__wrapped__)  # no device to switch to
+    return seen
+
+
+def test_a_differentiable_call_reports_forward_and_gradients(library):
+    q, k = torch.zeros(2, 8, 4, 64), torch.zeros(2, 8, 2, 64)
+    word = torch.zeros(2, dtype=torch.int32)
+    sg.softmax_attention.__wrapped__(q, k, k, device_status=word)
+    assert library == [("softmax_attention_fwd", word.data_ptr())]
+    library.clear()
+    q.requires_grad_()
+    o = sg.softmax_attention.__wrapped__(q, k, k, device_status=word)
+    torch.autograd.grad(o, q, torch.ones_like(o))
+    assert library == [("softmax_attention_fwd", word.data_ptr()), ("softmax_attention_bwd", word.data_ptr() + 4)]
+    library.clear()
+    o = sg.softmax_attention.__wrapped__(q, k, k)
+    torch.autograd.grad(o, q, torch.ones_like(o))
+    assert library == [("softmax_attention_fwd", None), ("softmax_attention_bwd", None)]
+    library.clear()
+    with pytest.raises(ValueError, match="2 elements"):  # no room for the gradients' status
+        sg.softmax_attention.__wrapped__(q, k, k, device_status=word[:1])
+    with pytest.raises(TypeError):
+        sg.softmax_attention.__wrapped__(q, k, k, device_status=word.long())
+    assert not library

@@ -41,3 +41,22 @@ def test_a_block_of_keys_that_takes_seconds():
     do[:, :-1] = 0
     r = sg.softmax_attention_bwd(q, k, v, o, lse, do, causal=False, device_status=status)
     assert int(status) == 0 and bool((r["dv"] == 1.0).all())
+
+
+def test_bad_bounds_show_through_the_differentiable_call():
+    gen = torch.Generator().manual_seed(1)
+    q, do = (torch.randn(100, 4, 64, generator=gen).to(BF16).cuda() for _ in range(2))
+    k, v = (torch.randn(100, 2, 64, generator=gen).to(BF16).cuda() for _ in range(2))
+    q.requires_grad_()
+    good, bad = (torch.tensor(x).cuda() for x in ([0, 50, 100], [0, 60, 50, 100]))
+    word = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+    o = sg.softmax_attention(q, k, v, cu_seqlens=good, device_status=word)
+    assert word.tolist() == [0, 9]
+    torch.autograd.grad(o, q, do)
+    assert word.tolist() == [0, 0]
+    o = sg.softmax_attention(q, k, v, cu_seqlens=bad, device_status=word)
+    assert word.tolist() == [1, 0]
+    torch.autograd.grad(o, q, do)
+    assert word.tolist() == [1, 1]
+    sg.softmax_attention(q.detach(), k, v, cu_seqlens=good, device_status=word[:1])
+    assert word.tolist() == [0, 1]
