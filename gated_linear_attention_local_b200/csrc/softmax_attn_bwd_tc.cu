@@ -449,7 +449,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
             auto row_value = [&](int i) -> float {
                 if (i >= n || rt >= R || i * R + rt >= it.q_left) return 0.f;
                 const int64_t row = row00 + (int64_t)i * R * a.H;
-                return w == 0 ? -kLog2e * a.lse_in[row] : -a.delta[row];
+                return w == 0 ? neg_lse(a.lse_in[row]) : -a.delta[row];
             };
             srow[(tile & 1) * 256 + threadIdx.x] = row_value(0);
             float next = row_value(1);
@@ -688,7 +688,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
             const bool mine = tr < R && tr < it.q_left;
             const int lim = mine ? max(0, a.causal ? min(it.keys, tr + 1 + it.shift) : it.keys) : 0;
             const int64_t row = mine ? (int64_t)(it.q_tok + tr) * a.H + it.hk * a.G + tg : 0;
-            const float lse = mine ? a.lse_in[row] * kLog2e : 0.f;
+            const float nlse = mine ? neg_lse(a.lse_in[row]) : 0.f;
             // delta = sum_d do o: a lane takes a 16-byte piece of a row, a warp 16 rows
             {
                 constexpr int PER = DP / 8, NK = 16 * PER / 32;
@@ -734,7 +734,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                 ld_pairs(cS + c0, p);
                 tc_fence_before();
                 mbar_arrive(b.sfree);
-                auto nl = [&](int) { return make_float2(-lse, -lse); };
+                auto nl = [&](int) { return make_float2(nlse, nlse); };
                 if (masked) exp_pass<true>(p, sc, nl, 0, left);
                 else exp_pass<false>(p, sc, nl, 0, left);
                 ok = ok && mbar_wait(&b.dp[tile & 1], (tile >> 1) & 1, abort_flag);

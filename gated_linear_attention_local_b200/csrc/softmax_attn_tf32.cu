@@ -111,6 +111,10 @@ __device__ __forceinline__ void copy_rows(float *tile, const float *src, int64_t
     }
 }
 
+// lse in units of log2, for p = 2^(s - lse).  -inf (the row saw nothing, or only scores of -inf): +inf, so
+// that all its p are 0.
+__device__ __forceinline__ float lse_log2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
 // First key that row r of a sequence must not see (keys [0, limit) are seen).
 __device__ __forceinline__ int64_t key_limit(const AttnArgs &a, const AttnTile &t, int64_t r, int64_t k_end) {
     if (r >= t.tq * a.G) return 0;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_dkdv_tf32_ker
             float x = 0.f;
             if (r < rows) {
                 const int64_t at = row_offset(t.q0, r, a.G, a.H, hk);
-                x = threadIdx.x < kB ? a.lse_in[at] * kLog2e : a.delta[at];
+                x = threadIdx.x < kB ? lse_log2(a.lse_in[at]) : a.delta[at];
             }
             srow[threadIdx.x] = x;
         }
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 64 ? 2 : 1) attn_dq_tf32_kerne
         const int64_t r = t.row0 + 16 * wr + 8 * h + (lane >> 2);
         lim[h] = key_limit(a, t, r, t.tk);
         const int64_t at = r < rows ? row_offset(t.q0, r, a.G, a.H, hk) : 0;
-        lse[h] = r < rows ? a.lse_in[at] * kLog2e : 0.f;
+        lse[h] = r < rows ? lse_log2(a.lse_in[at]) : 0.f;
         delta[h] = r < rows ? a.delta[at] : 0.f;
     }
     const int64_t seen = key_limit(a, t, min64(t.row0 + kB, rows) - 1, t.tk);

@@ -60,3 +60,42 @@ def test_bad_bounds_show_through_the_differentiable_call():
     assert word.tolist() == [1, 1]
     sg.softmax_attention(q.detach(), k, v, cu_seqlens=good, device_status=word[:1])
     assert word.tolist() == [0, 1]
+
+
+def operands(gen, dtype, Tq, Tk, H, Hk, D):
+    q, do = (torch.randn(1, Tq, H, D, generator=gen).to(dtype).cuda() for _ in range(2))
+    k, v = (torch.randn(1, Tk, Hk, D, generator=gen).to(dtype).cuda() for _ in range(2))
+    return q, k, v, do
+
+
+def rounding(dtype):
+    """One rounding of a result; fp32: with room for its sums."""
+    return 2.0 ** -8 if dtype == BF16 else 2.0 ** -16
+
+
+def minus_infinity(dtype):
+    gen = torch.Generator().manual_seed(2)
+    q, k, v, do = operands(gen, dtype, 200, 300, 4, 2, 64)
+    q[..., 0] = -1.0
+    k[..., 0] = 0.0
+    want, want_lse = sg.softmax_attention_fwd(q, k[:, 200:].contiguous(), v[:, 200:].contiguous(), causal=False)
+    k[:, :200, :, 0] = float("inf")
+    v[:, :200] = torch.finfo(dtype).max
+    o, lse = sg.softmax_attention_fwd(q, k, v, causal=False)
+    # the same 100 keys in one tile or in two: on each side p is rounded, and o
+    assert float((o.double() - want.double()).abs().max()) <= 4 * rounding(dtype) * float(v[:, 200:].abs().max())
+    assert float((lse - want_lse).abs().max()) <= 2e-4  # sums of p, each to 7.5e-5
+    k[..., 0] = float("inf")
+    o, lse = sg.softmax_attention_fwd(q, k, v, causal=False)
+    assert float(o.abs().max()) == 0.0 and bool((lse == float("-inf")).all())
+    v.zero_()
+    r = sg.softmax_attention_bwd(q, k, v, o, lse, do, causal=False)
+    assert float(r["dk"].abs().max()) == 0.0 and float(r["dv"].abs().max()) == 0.0
+    assert float(r["dq"][..., 1:].abs().max()) == 0.0
+
+
+def test_scores_of_minus_infinity_weigh_nothing():
+    """Keys whose score is -inf get the weight 0 in every tile, so values of any size there do not show; rows whose
+    visible scores are all -inf come out as rows that see nothing, and add nothing to dk and dv.  (The first column of dq
+    is 0 times the infinite key.)"""
+    minus_infinity(BF16)
