@@ -160,10 +160,10 @@ struct Rows<__nv_bfloat16, DP, GM> {
         uint32_t p[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float ms = m[h] == -INFINITY ? 0.f : m[h] * sc;
+            const float base = m[h] == -INFINITY ? 0.f : m[h];  // (the difference first: m sc rounds, and may be huge)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const float x = fast_exp2(fmaf(s[n][2 * h], sc, -ms)), y = fast_exp2(fmaf(s[n][2 * h + 1], sc, -ms));
+                const float x = fast_exp2((s[n][2 * h] - base) * sc), y = fast_exp2((s[n][2 * h + 1] - base) * sc);
                 l[h] += x + y;
                 p[2 * n + h] = pack_bf16(x, y);
             }

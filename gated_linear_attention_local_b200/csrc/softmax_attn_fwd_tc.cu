@@ -58,6 +58,10 @@ constexpr int kFwdThreads = 384;
 constexpr int kTile = 128;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 units the maximum may lag behind
+// sc S - m sc in one FMA carries the rounding of m sc, 2^-24 of it, in every p of the row alike.  That
+// cancels in o; where it could take p out of range (keys given the lowest value of their type) the
+// difference S - m is formed first.
+constexpr float kFar = 16777216.f;
 
 // What the roles need to know of a work item; every count fits 32 bits.
 struct Item {
@@ -355,6 +359,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const int n = w == 0 ? it.nt[0] : it.nt[1];
             const int lim = mine ? (a.causal ? min(it.keys, x + 1 + it.shift) : it.keys) : 0;  // keys the row sees
             float m = -INFINITY, l = 0.f;  // m in units of S
+            bool far = false;
             for (int j = 0; j < n; ++j, ++ns) {
                 if (!(ok = all_wait(&b_s[w], ns & 1, abort_flag))) break;
                 tc_fence_after();
@@ -388,6 +393,7 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 }
                 __syncwarp();
                 if (__any_sync(0xffffffffu, f != 1.f)) {
+                    far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * sc) > kFar);
                     l *= f;
                     if (j > 0) {
                         for (int c = 0; c < a.D; c += 16) {
@@ -402,7 +408,15 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                         tmem_wait_st();
                     }
                 }
-                const float ms = m == -INFINITY ? 0.f : m * sc;
+                float ms = m == -INFINITY ? 0.f : m * sc;
+                if (far) {
+                    const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[c][e] -= m0;
+                    ms = 0.f;
+                }
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 auto part = [&](int c) {
                     if (masked) probabilities<true>(s[c], sc, ms, cS + 16 * c, sum);

@@ -99,3 +99,46 @@ def test_scores_of_minus_infinity_weigh_nothing():
     visible scores are all -inf come out as rows that see nothing, and add nothing to dk and dv.  (The first column of dq
     is 0 times the infinite key.)"""
     minus_infinity(BF16)
+
+
+def equal_scores(dtype, value, decode):
+    """Every score is value / 8: o is the mean of the values."""
+    gen = torch.Generator().manual_seed(3)
+    q, k, v, _ = operands(gen, dtype, 1 if decode else 150, 333, 4, 2, 64)
+    k.zero_()
+    q[..., 0], k[..., 0] = 1.0, value
+    if decode:
+        o = sg.softmax_attention_decode_step(q[:, 0].contiguous(), k, v, torch.tensor([333]).cuda())[:, None]
+    else:
+        o, lse = sg.softmax_attention_fwd(q, k, v, causal=False)
+        score = float(k[0, 0, 0, 0].double()) / 8
+        assert float((lse.double() - score).abs().max()) <= 2.0 ** -20 * abs(score)
+    want = v.double().mean(1).repeat_interleave(2, 1)[:, None]
+    # p is 1 or a value near 1, the same up to 7.5e-5 for all keys; then o is rounded
+    assert float((o.double() - want).abs().max()) <= rounding(dtype) * float(v.double().abs().mean(1).max())
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("value", [-3.38e38, -1e30, 1e12, 2e38])
+def test_huge_equal_scores(value, decode):
+    """A row whose keys were all given the type's lowest value, or any huge one, is the mean of their values."""
+    equal_scores(BF16, value, decode)
+
+
+def lowest_then_ordinary(dtype):
+    gen = torch.Generator().manual_seed(4)
+    q, k, v, _ = operands(gen, dtype, 150, 400, 2, 1, 128)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    want, _ = sg.softmax_attention_fwd(q, k[:, 256:].contiguous(), v[:, 256:].contiguous(), causal=False)
+    k[:, :256, :, 0] = torch.finfo(dtype).min
+    o, _ = sg.softmax_attention_fwd(q, k, v, causal=False)
+    # the same 144 keys, whole tiles of others in front of them: on each side p is rounded, and o
+    off = 4 * rounding(dtype) * float(v.abs().max())
+    assert float((o.double() - want.double()).abs().max()) <= off
+    step = sg.softmax_attention_decode_step(q[:, 0].contiguous(), k, v, torch.tensor([400]).cuda())
+    assert float((step.double() - want[:, 0].double()).abs().max()) <= off
+
+
+def test_lowest_scores_then_ordinary_ones():
+    """Keys of the lowest value weigh nothing beside ordinary ones that come later, whatever their own tiles held."""
+    lowest_then_ordinary(BF16)
