@@ -54,8 +54,12 @@ struct Split {
     uint32_t hi, lo;
 };
 __device__ __forceinline__ Split split(float x) {
+    // |x| first cut to the largest 11-bit value: rounding would take values above it to infinity, and
+    // lo = x - hi to NaN.  (An infinity is then lo's.)
+    float cut;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(cut) : "f"(x), "f"(__uint_as_float(0x7f7fe000u)));
     Split s;
-    s.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    s.hi = (__float_as_uint(cut) + 0x1000u) & 0xffffe000u;
     s.lo = __float_as_uint(x - __uint_as_float(s.hi));
     return s;
 }

@@ -142,3 +142,30 @@ def lowest_then_ordinary(dtype):
 def test_lowest_scores_then_ordinary_ones():
     """Keys of the lowest value weigh nothing beside ordinary ones that come later, whatever their own tiles held."""
     lowest_then_ordinary(BF16)
+
+
+def test_fp32_operands_to_the_ends_of_their_range():
+    """The split of an fp32 operand into two parts holds for the largest finite values (which rounding to 11 bits takes
+    past the range) and for infinities."""
+    minus_infinity(FP32)
+    lowest_then_ordinary(FP32)
+    for decode in (False, True):
+        for value in (torch.finfo(FP32).min, -1e30, 1e12, torch.finfo(FP32).max):
+            equal_scores(FP32, value, decode)
+
+
+def test_fp32_largest_values_stay():
+    """A value of the largest size at the only key that a row sees is the output, and elsewhere reaches no row."""
+    top = torch.finfo(FP32).max
+    gen = torch.Generator().manual_seed(6)
+    q, k, v, _ = operands(gen, FP32, 70, 70, 2, 1, 32)
+    want, _ = sg.softmax_attention_fwd(q, k, v)
+    v[:, 69, 0, 3], v[:, 0, 0, 4] = top, -top
+    o, _ = sg.softmax_attention_fwd(q, k, v)
+    # row 0 sees key 0 alone: 1 times its value, a product of three parts, to 2^-21
+    assert float((o[0, 0, :, 4].double() / top + 1).abs().max()) <= 2.0 ** -21
+    keep = [c for c in range(32) if c != 4]
+    assert torch.equal(o[:, :69][..., keep], want[:, :69][..., keep])
+    # row 69 sees key 69 too: finite, p times the largest value, p of 70 terms to 2^-16
+    p = torch.softmax(torch.einsum("hd,jd->hj", q[0, 69].double(), k[0, :, 0].double()) / 32 ** 0.5, -1)[:, 69]
+    assert float((o[0, 69, :, 3].double() / top - p).abs().max()) <= 2.0 ** -16 * float(p.max())
