@@ -101,11 +101,13 @@ struct BwdBars {
     }
 };
 
-// Zero rows [from, 128) of a tile, by one warp.
+// Zero the rows outside [from, to) of a tile, by one warp.
 template <int NG>
-__device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int lane) {
-    for (int i = lane; i < NG * kTile * 8; i += 32)
-        if (((i >> 3) & (kTile - 1)) >= from) reinterpret_cast<uint4 *>(tile)[i] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_outside(unsigned char *tile, int from, int to, int lane) {
+    for (int i = lane; i < NG * kTile * 8; i += 32) {
+        const int r = (i >> 3) & (kTile - 1);
+        if (r < from || r >= to) reinterpret_cast<uint4 *>(tile)[i] = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async_smem();
     __syncwarp();
 }
@@ -265,6 +267,7 @@ struct KvItem {
     int k_left;  // keys of the sequence from there on
     int q_tok;   // first token of the first row tile
     int q_left;  // tokens of the sequence from there on
+    int lead;    // tokens at the head of the first row tile that see none of the keys
     int ahead;   // causal: row c of tile i sees key r iff c >= (ahead + r - i R) G
     int hk;
 };
@@ -296,7 +299,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
         mbar_fence_init();
     }
     if (R * a.G < kTile && warp < kStX + kStY)  // rows that no copy writes are operands too
-        zero_rows<C::NG>(sm + C::X0 + warp * C::T, R * a.G, lane);
+        zero_outside<C::NG>(sm + C::X0 + warp * C::T, 0, R * a.G, lane);
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -326,6 +329,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 it.k_left = (int)(t.tk - t.row0);
                 it.q_tok = (int)(t.q0 + b0 * R);
                 it.q_left = (int)(t.tq - b0 * R);
+                it.lead = it.n > 0 ? (int)(first - b0 * R) : 0;
                 it.ahead = a.causal ? (int)max(t.row0 - off - b0 * R, -(int64_t)INT_MAX / 2) : -INT_MAX / 2;
                 return true;
             });
@@ -367,8 +371,12 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                 // the same in every lane; the reduction leaves it in a uniform register
                 const int n = __reduce_max_sync(0xffffffffu, it.n);
                 if (n == 0) continue;
-                // rows of tile i that do not exist are zeroed: 0 * NaN must not arise
-                const int whole = it.q_left / R;  // tiles before the first partial one
+                // rows of a tile that do not exist, or see none of the keys, are zeroed: 0 * NaN must not arise
+                const int whole = it.q_left / R, lead = it.lead * a.G;  // tiles before the first partial one
+                auto clean = [&](unsigned char *tile, int i) {
+                    if (i >= whole || (i == 0 && lead > 0))
+                        zero_outside<C::NG>(tile, i == 0 ? lead : 0, i >= whole ? (it.q_left - i * R) * a.G : kTile, lane);
+                };
                 if (!(ok = wait(b.own, own_ph))) break;
                 own_ph ^= 1u;
                 // two blocks of products a tile, each issued without a pause (the pipe holds few
@@ -377,7 +385,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     const bool more = i + 1 < n;
                     if (more) {
                         if (!(ok = wait(&b.full_x[x1.s], x1.ph))) break;
-                        if (i + 1 >= whole) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                        clean(sm + C::X0 + x1.s * C::T, i + 1);
                     }
                     if (i >= 0 && !(ok = wait(b.p, ph))) break;
                     tc_fence_after();
@@ -394,7 +402,7 @@ attn_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constan
                     __syncwarp();
                     if (more) {
                         if (!(ok = wait(&b.full_y[y1.s], y1.ph))) break;
-                        if (i + 1 >= whole) zero_rows<C::NG>(sm + C::Y0 + y1.s * C::T, (it.q_left - (i + 1) * R) * a.G, lane);
+                        clean(sm + C::Y0 + y1.s * C::T, i + 1);
                     }
                     if (i >= 0 && !(ok = wait(&b.ds[0], ph))) break;
                     tc_fence_after();
@@ -631,7 +639,7 @@ attn_dq_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant_
                     if (i + 1 < n) {
                         wait(&b.full_x[x1.s], x1.ph);
                         const int left = it.keys - (i + 1) * kTile;  // keys behind the sequence are operands too
-                        if (left < kTile) zero_rows<C::NG>(sm + C::X0 + x1.s * C::T, left, lane);
+                        if (left < kTile) zero_outside<C::NG>(sm + C::X0 + x1.s * C::T, 0, left, lane);
                         wait(&b.full_y[y1.s], y1.ph);
                         wait(b.sfree, free_ph);  // (the very first passes at once)
                         free_ph ^= 1u;

@@ -169,3 +169,19 @@ def test_fp32_largest_values_stay():
     # row 69 sees key 69 too: finite, p times the largest value, p of 70 terms to 2^-16
     p = torch.softmax(torch.einsum("hd,jd->hj", q[0, 69].double(), k[0, :, 0].double()) / 32 ** 0.5, -1)[:, 69]
     assert float((o[0, 69, :, 3].double() / top - p).abs().max()) <= 2.0 ** -16 * float(p.max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("H", [1, 4, 7])
+def test_rows_that_see_nothing_may_hold_anything(dtype, H):
+    """Causal, more queries than keys: what the first rows hold (NaN, infinity) reaches no gradient."""
+    gen = torch.Generator().manual_seed(5)
+    q, k, v, do = operands(gen, dtype, 333, 200, H, 1, 64)
+    o, lse = sg.softmax_attention_fwd(q, k, v)
+    want = sg.softmax_attention_bwd(q, k, v, o, lse, do)
+    q[:, :133], do[:, :133] = float("nan"), float("-inf")
+    o2, lse2 = sg.softmax_attention_fwd(q, k, v)
+    got = sg.softmax_attention_bwd(q, k, v, o2, lse2, do)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
