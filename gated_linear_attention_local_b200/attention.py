@@ -243,7 +243,8 @@ def _rotary(q, k, positions, inv_freq, axes, interleaved, inverse, where):
         raise ValueError(f"inv_freq has {half} pairs, a head of {D} has {D // 2}")
     if isinstance(axes, int):
         raise TypeError("axes must be a sequence of ints")
-    table = bytes(half) if axes is None else bytes(axes)
+    # (element by element: bytes() of an array is its memory, of a one-element tensor that many zeros)
+    table = bytes(half) if axes is None else bytes(axes if type(axes) in (list, tuple) else list(axes))
     if len(table) != half or A > 255:  # an axis that is not below A is refused by the library
         raise ValueError(f"axes must hold one axis below {A} for each of the {half} pairs, {A} at most 255")
     qo = torch.empty_like(q)

@@ -1,5 +1,6 @@
 """What the bindings of softmax attention, rotary positions and the chunked mixer do around the library's call: no GPU
 is used, the calls are stood in for."""
+import numpy as np
 import pytest
 import torch
 from torch.autograd import forward_ad
@@ -82,3 +83,30 @@ def test_a_differentiable_call_reports_forward_and_gradients(library):
     with pytest.raises(TypeError):
         sg.softmax_attention.__wrapped__(q, k, k, device_status=word.long())
     assert not library
+
+
+@pytest.mark.parametrize("make", [list, tuple, bytes, lambda x: np.array(x, dtype=np.int64), lambda x: np.array(x, np.uint8),
+                                  torch.tensor, lambda x: range(len(x))])
+def test_axes_of_any_sequence(monkeypatch, make):
+    """What reaches the library is one byte a pair, the axis's number, whatever kind of sequence held it."""
+    seen = []
+
+    class Library:
+        @staticmethod
+        def multi_axis_rotary(*a):
+            seen.append(a[4])
+            return 0
+    monkeypatch.setattr(attention, "lib", Library)
+    monkeypatch.setattr(attention, "_stream", lambda: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    rotary = sg.multi_axis_rotary.__wrapped__
+    for half in (1, 2, 8):
+        axes = make(list(range(half)))
+        rotary(torch.zeros(3, 2, 2 * half), None, torch.zeros(3, 9, dtype=torch.int64), torch.ones(half), axes=axes)
+        assert seen.pop() == bytes(range(half))
+    for axes in (make([0, 1]), make([0])):  # another number of axes than pairs, however many bytes they take
+        with pytest.raises(ValueError):
+            rotary(torch.zeros(3, 2, 16), None, torch.zeros(3, 9, dtype=torch.int64), torch.ones(8), axes=axes)
+    one = make([0, 1])[1:2]
+    rotary(torch.zeros(3, 2, 2), None, torch.zeros(3, 2, dtype=torch.int64), torch.ones(1), axes=one)
+    assert seen.pop() == b"\x01"
