@@ -32,10 +32,20 @@ cudaError_t tc_make_map_rows(CUtensorMap *m, const void *ptr, int64_t tokens, in
     cuuint64_t strides[2] = {(cuuint64_t)D * es, (cuuint64_t)H * D * es};
     cuuint32_t boxd[3] = {f32 ? 32u : 64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                          const_cast<void *>(ptr), dims, strides, boxd, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto encode = [&] {
+        return g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void *>(ptr), dims, strides, boxd, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r != CUDA_SUCCESS) {
+        // A driver call needs the thread's context, and a thread has none before a runtime call of its
+        // own binds it: this may be its first (autograd runs gradients in a thread of its own).
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = cudaSetDevice(dev)) != cudaSuccess) return e;
+        r = encode();
+    }
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
