@@ -84,3 +84,40 @@ def test_gradients_before_anything_else_in_autograds_thread():
             "print('fine')\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("mixer", ["softmax", "packed"])
+def test_a_training_step_captured_and_replayed(mixer):
+    """Rotation and attention, forward and backward through autograd, in one graph; replayed on new inputs beside an
+    eager step on the same leaves."""
+    gen = torch.Generator().manual_seed(3)
+    lead = (2, 150) if mixer == "softmax" else (300,)
+    q, k, v, do = (torch.randn(*lead, h, 64, generator=gen).to(BF16).cuda() for h in (4, 2, 2, 4))
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    pos = torch.randint(0, 1000, (*lead, 2), generator=gen).cuda()
+    freq, axes = torch.rand(32, generator=gen).cuda(), [i % 2 for i in range(32)]
+    cu = None if mixer == "softmax" else torch.tensor([0, 100, 101, 300]).cuda()
+
+    def step():
+        qr, kr = sg.multi_axis_rotary(q, k, pos, freq, axes=axes)
+        o = sg.softmax_attention(qr, kr, v, cu_seqlens=cu)
+        return (o.detach(), *torch.autograd.grad(o, leaves, do))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        for x in (q, k, v, do):
+            x.copy_(torch.randn(x.shape, generator=gen).to(BF16))
+        pos.add_(5)
+    graph.replay()
+    want = step()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
