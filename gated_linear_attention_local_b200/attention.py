@@ -262,6 +262,7 @@ class MultiAxisRotaryFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, inv_freq, axes, interleaved):
         ctx.save_for_backward(positions, inv_freq)
+        axes = None if axes is None else bytes(list(axes))  # read once: the caller's sequence may change later
         ctx.opts = (axes, interleaved)
         return _rotary(q, k, positions, inv_freq, axes, interleaved, False, "multi_axis_rotary")
 

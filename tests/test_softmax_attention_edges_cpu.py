@@ -110,3 +110,24 @@ def test_axes_of_any_sequence(monkeypatch, make):
     one = make([0, 1])[1:2]
     rotary(torch.zeros(3, 2, 2), None, torch.zeros(3, 2, dtype=torch.int64), torch.ones(1), axes=one)
     assert seen.pop() == b"\x01"
+
+
+def test_axes_that_change_after_the_call(monkeypatch):
+    """The gradient turns by the axes of the call, whatever became of the caller's list."""
+    seen = []
+
+    class Library:
+        @staticmethod
+        def multi_axis_rotary(*a):
+            seen.append(a[4])
+            return 0
+    monkeypatch.setattr(attention, "lib", Library)
+    monkeypatch.setattr(attention, "_stream", lambda: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    monkeypatch.setattr(attention, "multi_axis_rotary_bwd", sg.multi_axis_rotary_bwd.__wrapped__)
+    axes = [0, 1, 2, 3]
+    q = torch.zeros(3, 2, 8, requires_grad=True)
+    o, _ = sg.multi_axis_rotary.__wrapped__(q, None, torch.zeros(3, 4, dtype=torch.int64), torch.ones(4), axes=axes)
+    axes.reverse()
+    torch.autograd.grad(o, q, torch.ones_like(o))
+    assert seen == [bytes(range(4))] * 2
