@@ -109,9 +109,11 @@ DecodePlan decode_plan(int64_t N, int64_t S, int64_t P, int64_t H, int64_t Hk, i
     const int64_t target = dtype == SGLA_BF16 ? 148 : 2 * 148;
     p.stream = G <= kDecodeMaxGroup;
     if (p.stream) {
-        // Few units: as many CTAs as run at once (two an SM; a second wave would double the
-        // time), at least 128 keys each.  Many: at least four waves, so that unequal lengths
-        // even out, at least 512 keys each (a CTA's fixed cost is some 5 us).
+        // Few units: up to eight CTAs each (one cluster), no more than run at once (two an SM; a
+        // second wave would double the time), at least 128 keys each.  Below 37 units that leaves
+        // SMs idle however long the cache is: one of 131072 keys takes 187 us on 8 key heads (64
+        // CTAs, 82 us at the copy rate) and on one (8 CTAs).  Many: at least four waves, so that
+        // unequal lengths even out, at least 512 keys each (a CTA's fixed cost is some 5 us).
         const int64_t units = N * Hk;
         while (p.cluster < 8 && ((units * p.cluster * 2 <= 2 * 148 && S >= 256 * p.cluster) ||
                                  (units > 148 && units * p.cluster < 8 * 148 && S >= 1024 * p.cluster)))

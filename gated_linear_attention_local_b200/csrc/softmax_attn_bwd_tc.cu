@@ -12,7 +12,7 @@
 //   S^T = K Q^T, dP^T = V dO^T   (128 keys x 128 rows, fp32, tensor memory; a lane a key)
 //   dV += P^T dO,  dK += dS^T Q  (P^T, dS^T in bf16 over S^T's and dP^T's columns)
 // issued as dV(i), S(i+1), dK(i), dP(i+1): p of tile i+1 is formed under dK(i) and dP(i+1), ds
-// under dV(i+1) and S(i+2), with one buffer each (tensor memory is full: 4 x 128 columns).
+// under dV(i+1) and S(i+2), with one buffer each (with heads of 128 tensor memory is full: 4 x 128 columns).
 // dq: one CTA owns 128 packed rows and walks the keys they see in tiles of 128:
 //   S = Q K^T, dP = dO V^T, dQ += dS K   (a lane a row)
 // issued as S(i+1), dP(i+1), dQ(i); dP has two buffers (dS lies over dP).
@@ -30,10 +30,12 @@
 // an item: the three kernels of packed training 500 -> 427 us when it came): the copies and first
 // products of an item run under the stores of the one before.
 //
-// Measured: 2 x 4096 causal tokens, 16 heads of 128 on 4: dq 176 us, dk dv 221 us (the forward
-// 127); 13 packed sequences of up to 2047 tokens, 12 heads of 64: 135 and 167 us (101).  Bound by
-// the chain of a tile (scores, p, ds, sums) through one buffer of each in tensor memory; heads of
-// 64 besides by products of 64 columns, which take as long as 128.
+// Measured (events around the launch, cold L2, less the 5 us that an empty pair of events reads):
+// 2 x 4096 causal tokens, 16 heads of 128 on 4: dq 187 us, dk dv 231 us (the forward 130); 13 packed
+// sequences of up to 2047 tokens, 12 heads of 64: 129 and 164 us (105).  Bound by the chain of a
+// tile (scores, p, ds, sums) through one buffer of each in tensor memory (dk dv: it is full for heads
+// above 64; up to 64 a quarter of it lies unused); heads of 64 besides by products of 64
+// columns, which take as long as 128.
 //
 // Shared memory (DP = 128): the item's own two tiles 64 KB, rings of three X tiles (Q or K, read
 // by the first and the last product of a tile) and two Y tiles (dO or V), 160 KB.
@@ -210,7 +212,8 @@ __device__ __forceinline__ void produce(unsigned char *sm, const BwdBars &b, con
     Ring<kStX> rx;
     Ring<kStY> ry;
     bool ok = true;
-    // (what a product warp that gave up released is not filled again)
+    // (one lane waits and copies, the others meet it at the shuffle behind an item's copies: nothing between
+    // is warp-wide; what a product warp that gave up released is not filled again)
     auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait_idle(bar, ph, abort_flag) && !*abort_flag; };
     while (ok && feed.take(ni, it)) {
         if (lane == 0 && it.n > 0) {

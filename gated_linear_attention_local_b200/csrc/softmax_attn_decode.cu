@@ -15,9 +15,10 @@
 // product's A operand as they stand.  p is rounded to bf16 for that product.
 // fp32: FMA on the CUDA cores; two lanes a key for the scores, a lane four (two) columns of v.
 //
-// Measured (bf16, 32 heads of 128 on 8): 128 caches of up to 4096 tokens (1.08 GB) 172 to 182 us, 91
-// to 96 % of the measured copy rate; 64 caches of up to 512 tokens 26 us behind a prefix, where a
-// CTA's fixed cost (some 5 us) and the join of the prefix's parts outweigh the 10 us of the stream.
+// Measured (bf16, 32 heads of 128 on 8; cold L2, less the 5 us that an empty pair of events reads): 128
+// caches of up to 4096 tokens (1.08 GB) 170 to 182 us, 91 to 97 % of the measured copy rate; 64 caches
+// of up to 512 tokens 26 us behind a prefix, where a CTA's fixed cost (some 5 us) and the join of the
+// prefix's parts outweigh the 10 us of the stream.
 //
 // Keys behind the valid length may hold anything: scores there are -inf, and the value rows of
 // the last tile are zeroed in shared memory (0 * NaN must not arise).

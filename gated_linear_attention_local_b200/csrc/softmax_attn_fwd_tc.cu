@@ -16,22 +16,23 @@
 // products of an item run under the epilogue of the one before, and unequal items even out
 // (against a fixed share of the items for each CTA: 8 packed prompts 269 -> 206 us when it came).
 //
-// Measured, heads of 128, causal: 8192 tokens of 32 heads on 8, 441 us = 1247 TFLOP/s (88 % of
-// the library's sustained rate: the power limit is near); 8 packed prompts of 128 to 4096 tokens,
-// 16 heads on 4, 178 us; 4 x 2048 tokens of 16 heads, 88 us.  What bounds it: the chain of a row
-// tile, scores -> probabilities -> P V -> next scores, of which two run side by side.  Without
-// exponentials, sums and maxima (for timing only) the first takes 399 us and the last 79, so the
-// softmax costs a tenth; a tile pair takes some 3000 cycles for the 2048 of its products, an
-// item's end 5500.
+// Measured (events around the launch, cold L2, less the 5 us that an empty pair of events reads),
+// heads of 128, causal: 8192 tokens of 32 heads on 8, 457 us = 1203 TFLOP/s alone (85 % of the
+// library's sustained rate; back to back, under the power limit, 535 us = 1028); 8 packed prompts of
+// 128 to 4096 tokens, 16 heads on 4, 187 us; 4 x 2048 tokens of 16 heads, 88 us.  What bounds it: the
+// chain of a row tile, scores -> probabilities -> P V -> next scores, of which two run side by side.
+// Without exponentials, sums and maxima (for timing only, at 436 and 84 us) the first took 399 us
+// and the last 79, so the softmax costs a tenth; a tile pair takes some 3000 cycles for the 2048 of
+// its products, an item's end 5500.
 //
 // The maximum m of a row is only moved (and O, l rescaled, in tensor memory, by the row's own
 // thread) when it has grown by more than 2^8: until then p <= 2^8, which fp32 sums and the
 // bf16 range (the rounding is relative) carry without loss.
 //
 // Exponentials: 128 x 128 of them take the special-function unit as long as the two products
-// take the tensor cores (1024 cycles), so a quarter goes to the FMA pipe instead
-// (softmax_attn_tc.cuh; 8192 tokens: 450 us with none, 447 with a quarter, 453 with three eighths).  A NaN among a row's visible scores makes its maximum and so all its p
-// NaN.
+// take the tensor cores (1024 cycles), so a quarter goes to the FMA pipe instead (softmax_attn_tc.cuh;
+// 8192 tokens, when it came: 450 us with none, 447 with a quarter, 453 with three eighths).  A NaN
+// among a row's visible scores makes its maximum and so all its p NaN; a score of -inf weighs 0.
 //
 // p is rounded to bf16 for the product with V (relative 2^-8, averaged over the keys); its sum
 // l, m, S and O are fp32.
@@ -205,7 +206,9 @@ attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             Item it;
             int ni = 0, kv = 0, nv = 0, nq[2] = {0, 0};
             bool ok = true;
-            // (what a product warp that gave up released is not filled again)
+            // One lane waits and copies, the others meet it at the shuffle behind an item's copies: nothing
+            // between is warp-wide.  (All lanes in the loop, an elected one copying: 470 -> 478 us at 8192
+            // tokens of 32 heads.)  What a product warp that gave up released is not filled again.
             auto wait = [&](uint64_t *bar, uint32_t ph) { return mbar_wait_idle(bar, ph, abort_flag) && !*abort_flag; };
             while (ok && feed.take(ni, it)) {
                 if (lane == 0) {

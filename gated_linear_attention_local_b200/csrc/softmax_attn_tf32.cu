@@ -18,8 +18,9 @@
 //
 // A cluster of up to 8 CTAs shares a tile where there are fewer tiles than SMs: each takes a part
 // of the keys (dk dv: of the rows), and the parts are joined through distributed shared memory
-// in a fixed order (2 x 317 queries and 501 keys, 8 heads of 64 on 4: 203 -> 143 us a training pass, with two
-// CTAs an SM up to D = 64; what is left is latency: four launches, and 2 to 8 tiles a CTA in turn).
+// in a fixed order (2 x 317 queries and 501 keys, 8 heads of 64 on 4: 203 -> 143 us a training pass when it
+// came, with two CTAs an SM up to D = 64; now 150, with operands split safely to the ends of their range.
+// What is left is latency: four launches, and 2 to 8 tiles a CTA in turn).
 //
 // The scores' accumulators are the next product's A operand as they stand: columns 2 t and
 // 2 t + 1 of an accumulator are taken as k = t and k = t + 4, and the B operand's rows are read in

@@ -522,7 +522,16 @@ SGLA_API sgla_status simple_gla_normalized_decode_step(const void *q, const void
  *   scale as simple_gla_fwd (NaN or <= 0 selects 1/sqrt(D)).
  * Only what a query sees is meant to be finite for its output to be; a value that is not
  * finite in a key or value later in the same tile of 128 keys can reach a causal query as
- * NaN (0 times it).  Keys behind a sequence's end are never read into a result.
+ * NaN (0 times it).  Keys behind a sequence's end are never read into a result, and rows of q
+ * and dout that see no key may hold anything.  A score of -inf weighs 0; a query that sees
+ * nothing else counts as one that sees no key.  Scores may have any finite size, and equal
+ * ones weigh alike.  lse, from which the gradients form p again, holds a row's sum to 2^-24 of
+ * itself: with scores of magnitude M p is known to some 2^-22 M of itself there (and between a
+ * prefix and a cache of the one-token step).
+ * Sums are fp32.  o is summed before it is divided by the sum of the weights (up to 2^8 a key), so
+ * values near the type's largest overflow where they weigh.  An accumulator of the tensor cores
+ * drops terms below 2^-25 of it: dk and dv of keys that more than 2^25 rows see, and o of rows
+ * that see as many keys, lose accuracy.
  * Supported sizes: D <= 128 and a multiple of 8, H a multiple of Hk, H / Hk <= 128,
  * H <= 65535, fewer than 2^30 tokens.  Tensor pointers 16-byte aligned.
  * Results do not depend on the order in which thread blocks run (no atomics).
