@@ -158,7 +158,9 @@ def softmax_attention(q, k, v, causal=True, scale=None, cu_seqlens=None, cu_seql
     """The output of softmax_attention_fwd alone; differentiable in q, k and v (through softmax_attention_bwd) when
     gradients are enabled and one of them requires gradients.  device_status: optional int32 CUDA tensor that receives
     what the device finds (sequences whose bounds are bad are skipped, their outputs and gradients not written): element
-    0 the forward's status, element 1 the gradients' once they run (it is needed when the call is differentiable)."""
+    0 the forward's status, element 1 the gradients' once they run (it is needed when the call is differentiable).
+    Forward and gradients can be captured into a graph, as long as no graph that autograd recorded eagerly from the same
+    leaves is alive then (torch refuses that for every operator)."""
     if _autograd_follows(q, k, v):
         return SoftmaxAttentionFunction.apply(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status)
     return _forward(q, k, v, causal, scale, cu_seqlens, cu_seqlens_k, device_status, want_lse=False)[0]

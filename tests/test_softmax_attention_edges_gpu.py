@@ -185,3 +185,44 @@ def test_rows_that_see_nothing_may_hold_anything(dtype, H):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_what_a_row_sees_that_is_no_number_shows(dtype):
+    """NaN in a query is its row's, NaN in a key every row's that sees it, and no other's."""
+    gen = torch.Generator().manual_seed(7)
+    q, k, v, _ = operands(gen, dtype, 300, 300, 4, 2, 64)
+    want, want_lse = sg.softmax_attention_fwd(q, k, v)
+    q2, k2 = q.clone(), k.clone()
+    q2[0, 7, 1, 5] = float("nan")
+    o, lse = sg.softmax_attention_fwd(q2, k, v)
+    hit = torch.zeros(1, 300, 4, dtype=torch.bool, device="cuda")
+    hit[0, 7, 1] = True
+    assert bool(o[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    k2[0, 150, 0, 63] = float("nan")
+    o, lse = sg.softmax_attention_fwd(q, k2, v)
+    hit = torch.zeros(1, 300, 4, dtype=torch.bool, device="cuda")
+    hit[0, 150:, :2] = True
+    assert bool(o[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    n = torch.tensor([150, 151]).cuda()
+    first = q[0, :2].contiguous()
+    cache = [x.expand(2, 300, 2, 64).contiguous() for x in (k2, v)]
+    step = sg.softmax_attention_decode_step(first, *cache, n)
+    assert bool(step[1, :2].isnan().all()) and bool(step[1, 2:].isfinite().all()) and bool(step[0].isfinite().all())
+    behind = sg.softmax_attention_decode_step(first, cache[0][:, :100].contiguous(), cache[1][:, :100].contiguous(),
+                                              torch.tensor([0, 100]).cuda(), cache[0][0], cache[1][0])
+    assert bool(behind[:, :2].isnan().all()) and bool(behind[:, 2:].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("B,T,S", [(0, 5, 5), (2, 0, 7), (2, 7, 0), (1, 0, 0)])
+def test_nothing_to_do(B, T, S, dtype):
+    """Empty sides, through the differentiable call: empty or zero results, no error."""
+    q, k = (torch.zeros(B, n, h, 64, device="cuda", dtype=dtype, requires_grad=True) for n, h in ((T, 4), (S, 2)))
+    v = torch.randn(B, S, 2, 64, device="cuda").to(dtype).requires_grad_()
+    o = sg.softmax_attention(q, k, v)
+    g = torch.autograd.grad(o, (q, k, v), torch.ones_like(o))
+    for got, like in ((o, q), (g[0], q), (g[1], k), (g[2], v)):
+        assert got.shape == like.shape and float(got.detach().abs().sum()) == 0.0
