@@ -66,7 +66,7 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatil
 }
 
 // A wait that lasts as long as an item, and an item may have any number of tiles (a wait for one tile
-// is bounded by itself): gives up when no copy has been issued for the limit, or another thread gave
+// is bounded by itself): gives up when `copies` stood still for the limit, or another thread gave
 // up.  IDLE: off the critical path, sleeps in the barrier.
 template <bool IDLE>
 __device__ __forceinline__ bool item_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, volatile int *copies) {
@@ -102,7 +102,7 @@ struct Feed {
     void *answer;                   // 16 bytes, 16-byte aligned
     Item *item;
     volatile int *abort_flag;
-    volatile int *copies;           // tiles copied so far (written by the copying lane)
+    volatile int *copies;           // changes with every tile copied and every block looked at
 
     __device__ void init() const {
         *abort_flag = 0;
@@ -138,6 +138,7 @@ struct Feed {
         };
         for (int u = blockIdx.x, asked = 0; ok && u >= 0;) {
             Item it;
+            *copies = u;  // (blocks without work may come in long runs: that is progress, too)
             if (describe(u, it)) {
                 publish(it);
                 if (!ok || !(ok = __all_sync(0xffffffffu, item_wait<true>(want, (count - 1) & 1, abort_flag, copies)))) break;

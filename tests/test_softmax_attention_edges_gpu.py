@@ -226,3 +226,25 @@ def test_nothing_to_do(B, T, S, dtype):
     g = torch.autograd.grad(o, (q, k, v), torch.ones_like(o))
     for got, like in ((o, q), (g[0], q), (g[1], k), (g[2], v)):
         assert got.shape == like.shape and float(got.detach().abs().sum()) == 0.0
+
+
+def test_a_pack_of_very_many_empty_sequences():
+    """2^27 sequences, all but the last empty: a CTA passes hundreds of thousands of blocks without work (some seconds)
+    between two items."""
+    N = 1 << 27
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of device memory")
+    gen = torch.Generator().manual_seed(8)
+    q, k, v, do = operands(gen, BF16, 128, 128, 1, 1, 64)
+    want, lse = sg.softmax_attention_fwd(q, k, v)
+    grads = sg.softmax_attention_bwd(q, k, v, want, lse, do)
+    cu = torch.zeros(N + 1, dtype=torch.int64, device="cuda")
+    cu[N] = 128
+    status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    o, lse2 = sg.softmax_attention_fwd(q, k, v, cu_seqlens=cu, device_status=status)
+    assert int(status) == 0
+    assert torch.equal(o, want) and torch.equal(lse, lse2)
+    got = sg.softmax_attention_bwd(q, k, v, o, lse, do, cu_seqlens=cu, device_status=status)
+    assert int(status) == 0
+    for n in grads:
+        assert torch.equal(got[n], grads[n]), n
