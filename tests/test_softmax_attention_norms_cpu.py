@@ -25,7 +25,7 @@ def test_roundings_stay_inside(case):
         assert norms.off(got[n], want[n]) <= norms.LIMIT[BF16], n
 
 
-@pytest.mark.parametrize("spoil,shows", [(("delta", 0.0), ("dq", "dk")), (("delta", 0.75), ("dq", "dk")),
+@pytest.mark.parametrize("spoil,shows", [(("delta", 0.0), ("dq", "dk")), (("delta", 0.75), ("dq", "dk")), (("delta", 0.9), ("dq", "dk")),
                                          (("delta", 1.25), ("dq", "dk")), (("tile", 0), ("dq",)), (("tile", 1), ("dq",)),
                                          (("p", 0), ("dv",))])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}x{c[1]}")
