@@ -67,7 +67,7 @@ struct BwdCfg {
     static constexpr uint32_t X0 = 2 * T, Y0 = X0 + kStX * T;
     static constexpr uint32_t ROWS = Y0 + kStY * T;  // [2][128] -lse (log2 units), [128] -delta of a tile's rows
     static constexpr uint32_t BARS = ROWS + 2 * 256 * 4;
-    static constexpr uint32_t MISC = BARS + 26 * 8;  // tensor memory address, abort flag, copies so far, 16 bytes of the feed
+    static constexpr uint32_t MISC = BARS + 26 * 8;  // tensor memory address, abort flag, the feed's progress and answer
     static constexpr uint32_t ITEM = MISC + 32;
     // (no slack for alignment: the array is declared with it)
     static constexpr size_t SMEM = ITEM + 64 > 120 * 1024 ? ITEM + 64 : 120 * 1024;

@@ -1,5 +1,8 @@
 """The first call that a host thread makes: a thread has no CUDA context until a runtime call of its own binds one, and
 autograd runs gradients in a thread of its own."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -73,8 +76,6 @@ def test_first_call_of_a_thread(name, dtype):
 
 def test_gradients_before_anything_else_in_autograds_thread():
     """A process whose first differentiable call is this one (a fresh process: autograd's thread outlives a test)."""
-    import subprocess
-    import sys
     code = ("import torch, gated_linear_attention_local_b200 as sg\n"
             "x = [torch.randn(1, 300, 2, 64, device='cuda', dtype=torch.bfloat16, requires_grad=True) for _ in range(3)]\n"
             "o = sg.softmax_attention(*x)\n"
@@ -82,7 +83,8 @@ def test_gradients_before_anything_else_in_autograds_thread():
             "torch.cuda.synchronize()\n"
             "assert all(bool(t.isfinite().all()) for t in g)\n"
             "print('fine')\n")
-    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
